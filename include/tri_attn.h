@@ -351,6 +351,167 @@ size_t tri_gate_bwd_workspace_bytes(int R);
 
 tri_attn_status tri_gate_bwd(const tri_gate_bwd_args *args, tri_attn_stream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * The pair block's per-position steps around the attention (no counterpart on
+ * the pages, which describe the attention itself): the layer norm in front of
+ * it, an 8-bit form of an activation kept for the backward pass, and a learned
+ * relative position bias in the layout the attention reads.  Ownership,
+ * asynchrony, determinism and error rules as for the other calls.
+ *
+ * Element types: a field named *_type holds TRI_TYPE_BF16 or TRI_TYPE_F32
+ * (else TRI_ATTN_ERR_DTYPE).  Rows are R rows of C channels with channel
+ * stride 1 and the given row stride in elements: any stride of at least C for
+ * what is written (so that rows do not overlap), any non-negative stride for
+ * what is read.  Pointers need the alignment of their element type only;
+ * 32-byte aligned data with row strides of a multiple of 32 bytes and C a
+ * multiple of 16 runs fastest.  Outputs do not overlap inputs.  Channels past
+ * C and rows past R are left as they were.  Sizes: 0 <= R (nothing to do at
+ * 0, except that weight gradients are written as zeros), 1 <= C <= 8192.
+ */
+#define TRI_TYPE_BF16 0
+#define TRI_TYPE_F32 1
+
+#define TRI_ACT8_NONE 0
+#define TRI_ACT8_INT8 1 /* codes are two's complement, -127 .. 127                  */
+#define TRI_ACT8_E4M3 2 /* codes are e4m3 floats (no infinities), largest 448        */
+
+/* Channels that share a scale: blocks start at multiples of 32 of a row, the
+ * last one may be cut short by C. */
+#define TRI_ACT8_BLOCK 32
+
+/* An activation in 8 bits: codes [R,C] (one byte each, row stride in bytes)
+ * and exponents [R, ceil(C/32)] (one byte each, row stride in bytes), both
+ * with unit inner stride.  A block with largest magnitude m is stored under
+ * the scale 2^e, e the least integer >= -126 with m <= Q 2^e, where Q = 127
+ * (INT8) or 448 (E4M3); its exponent byte is e + 127.  Each code is the
+ * nearest one to value / 2^e, ties to even, and stands for code * 2^e.  A
+ * block that holds an infinity or a NaN gets the exponent byte 255 and codes
+ * 0, and is restored as NaNs.  (Magnitudes within a code's half step of 2^128
+ * are restored as 2^128, which is an infinity in both element types.)  kind TRI_ACT8_NONE: no activation is given. */
+typedef struct {
+    void *codes;
+    int64_t codes_stride;
+    void *exps;
+    int64_t exps_stride;
+    int kind;
+} tri_act8;
+
+/* Layer norm over the channels of each row, forward:
+ *     mean = sum_c x / C,  rstd = 1 / sqrt(sum_c (x - mean)^2 / C + eps),
+ *     y = (x - mean) * rstd * w + b
+ *   x     : [R,C] input;  w, b : contiguous [C] of type w_type, either may be
+ *           NULL (1 and 0)
+ *   y     : [R,C] output, rounded once from FP32
+ *   stats : FP32, contiguous [2,R] output: the R means, then the R rstds
+ *   act   : TRI_ACT8_NONE, or an output: x in 8 bits, for tri_norm_restore,
+ *           tri_norm_bwd and tri_act8_unpack
+ *   eps   : finite, not negative */
+typedef struct {
+    int64_t R;
+    const void *x;
+    int64_t x_stride;
+    const void *w, *b;
+    void *y;
+    int64_t y_stride;
+    float *stats;
+    tri_act8 act;
+    int C, x_type, w_type, y_type;
+    float eps;
+} tri_norm_fwd_args;
+
+tri_attn_status tri_norm_fwd(const tri_norm_fwd_args *args, tri_attn_stream_t stream);
+
+/* y of tri_norm_fwd once more, from what was kept of x: act and stats are
+ * read, y is written; x, x_type and eps are not used. */
+tri_attn_status tri_norm_restore(const tri_norm_fwd_args *args, tri_attn_stream_t stream);
+
+/* Layer norm, backward, with h = (x - mean) * rstd and g = dy * w:
+ *     dx = rstd * (g - mean_c(g) - h * mean_c(g h)),
+ *     dw = sum_r dy h,   db = sum_r dy
+ *   f      : the forward's R, C, w, w_type, stats, and x with x_type, or, with
+ *            f.act.kind set, act in place of x (f.x is then not used); b, y and
+ *            eps are not used
+ *   dy     : [R,C] upstream gradient of type f.y_type
+ *   dx     : [R,C] output of type f.x_type, or NULL
+ *   dw, db : FP32 contiguous [C] outputs, or both NULL
+ *   workspace, workspace_bytes : caller-owned device scratch of at least
+ *            tri_norm_bwd_workspace_bytes(R, C) bytes, 16-byte aligned; not
+ *            used when dw and db are NULL */
+typedef struct {
+    tri_norm_fwd_args f;
+    const void *dy;
+    int64_t dy_stride;
+    void *dx;
+    int64_t dx_stride;
+    float *dw, *db;
+    void *workspace;
+    size_t workspace_bytes;
+} tri_norm_bwd_args;
+
+/* Bytes of workspace tri_norm_bwd needs (pure function of the sizes; 0 for
+ * invalid ones). */
+size_t tri_norm_bwd_workspace_bytes(int64_t R, int C);
+
+tri_attn_status tri_norm_bwd(const tri_norm_bwd_args *args, tri_attn_stream_t stream);
+
+/* act = x in 8 bits; x [R,C] of type x_type with the given row stride. */
+tri_attn_status tri_act8_pack(int64_t R, int C, const void *x, int64_t x_stride, int x_type, tri_act8 act,
+                              tri_attn_stream_t stream);
+/* x = the values act stands for, rounded to x_type. */
+tri_attn_status tri_act8_unpack(int64_t R, int C, tri_act8 act, void *x, int64_t x_stride, int x_type,
+                                tri_attn_stream_t stream);
+
+/* Learned relative position bias by buckets.  For batch b, query i, key j:
+ *     delta  = pos_k[b,j] - pos_q[b,i]
+ *     bucket = number of e with edges[e] <= delta                  (0 .. E)
+ *              or E + 1, where groups are given and group_q[b,i] != group_k[b,j]
+ *     bias[b,h,i,j] = table[bucket,h] (+ base[b,h,i,j])
+ *   edges   : int32 [E], ascending (equal ones allowed), above -2^31;
+ *             1 <= E <= 510
+ *   pos_*   : int32 [B,Nq] and [B,Nk], unit inner stride, the given batch
+ *             strides (0: shared by the batch); differences may pass 32 bits
+ *   group_* : int32, laid out as pos_* with the same batch strides (chains,
+ *             segments), or both NULL
+ *   table   : [E + 1, H], or [E + 2, H] with groups; contiguous, of type table_type
+ *   base    : BF16 [B,H,Nq,Nk] or ptr NULL;  bias : BF16 [B,H,Nq,Nk] output,
+ *             rounded once from the FP32 sum.  Strides as for the attention's
+ *             bias: innermost 1, the others non-negative multiples of 8
+ *             elements, pointers 16-byte aligned; the bias's own rows must not
+ *             overlap.  Elements of a padded row past Nk are left as they were.
+ * Sizes: 1 <= B, H, Nq, Nk, with B * Nq * ceil(Nk/8) < 2^31 and H <= 4096. */
+typedef struct {
+    int B, H, Nq, Nk, E, table_type;
+    const void *table;
+    const int32_t *edges;
+    const int32_t *pos_q, *pos_k;
+    const int32_t *group_q, *group_k;
+    int64_t q_stride, k_stride;
+    tri_attn_tensor4 base;
+    tri_attn_tensor4 bias;
+} tri_relpos_fwd_args;
+
+tri_attn_status tri_relpos_fwd(const tri_relpos_fwd_args *args, tri_attn_stream_t stream);
+
+/* Gradient of the table: dtable[k,h] = sum over b, i, j of bucket k of
+ * dbias[b,h,i,j], FP32, contiguous, shaped as the table.
+ *   f     : the forward's sizes, edges, positions and groups (table, base and
+ *           bias are not used)
+ *   dbias : BF16 [B,H,Nq,Nk], strides as for base
+ *   workspace : caller-owned device scratch of at least
+ *           tri_relpos_bwd_workspace_bytes(...) bytes, 16-byte aligned */
+typedef struct {
+    tri_relpos_fwd_args f;
+    tri_attn_tensor4 dbias;
+    float *dtable;
+    void *workspace;
+    size_t workspace_bytes;
+} tri_relpos_bwd_args;
+
+/* groups: nonzero if groups are given.  Pure function; 0 for invalid sizes. */
+size_t tri_relpos_bwd_workspace_bytes(int B, int H, int Nq, int Nk, int E, int groups);
+
+tri_attn_status tri_relpos_bwd(const tri_relpos_bwd_args *args, tri_attn_stream_t stream);
+
 /* Static, NUL-terminated description of a status code. */
 const char *tri_attn_strerror(tri_attn_status status);
 

@@ -18,3 +18,20 @@ from ._binding import (  # noqa: F401
     tri_attn_strerror,
 )
 from .api import backward, forward, triangle_attention  # noqa: F401
+from .norm import (  # noqa: F401
+    Act8,
+    act8_pack,
+    act8_unpack,
+    layer_norm,
+    norm_backward,
+    norm_forward,
+    norm_linear,
+    norm_restore,
+)
+from .relpos import (  # noqa: F401
+    relative_position_bias,
+    relpos_backward,
+    relpos_edges_clipped,
+    relpos_edges_log,
+    relpos_forward,
+)

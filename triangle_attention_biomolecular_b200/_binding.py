@@ -30,6 +30,9 @@ TRI_ATTN_ERR_DEVICE_TIMEOUT = 10
 TRI_ATTN_ERR_SCRATCH_LIMIT = 11
 TRI_ATTN_STATIC_SCRATCH_BYTES = 64 << 20
 TRI_ATTN_BWD_NO_RESIDUAL = 1
+TRI_TYPE_BF16, TRI_TYPE_F32 = 0, 1
+TRI_ACT8_NONE, TRI_ACT8_INT8, TRI_ACT8_E4M3 = 0, 1, 2
+TRI_ACT8_BLOCK = 32
 
 
 class TriAttnError(RuntimeError):
@@ -86,12 +89,52 @@ class BwdArgs(ctypes.Structure):
                 ("flags", ctypes.c_uint)]
 
 
+class Act8(ctypes.Structure):
+    _fields_ = [("codes", ctypes.c_void_p), ("codes_stride", ctypes.c_int64), ("exps", ctypes.c_void_p),
+                ("exps_stride", ctypes.c_int64), ("kind", ctypes.c_int)]
+
+
+class NormFwdArgs(ctypes.Structure):
+    _fields_ = [("R", ctypes.c_int64), ("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64), ("w", ctypes.c_void_p),
+                ("b", ctypes.c_void_p), ("y", ctypes.c_void_p), ("y_stride", ctypes.c_int64),
+                ("stats", ctypes.c_void_p), ("act", Act8), ("C", ctypes.c_int), ("x_type", ctypes.c_int),
+                ("w_type", ctypes.c_int), ("y_type", ctypes.c_int), ("eps", ctypes.c_float)]
+
+
+class NormBwdArgs(ctypes.Structure):
+    _fields_ = [("f", NormFwdArgs), ("dy", ctypes.c_void_p), ("dy_stride", ctypes.c_int64), ("dx", ctypes.c_void_p),
+                ("dx_stride", ctypes.c_int64), ("dw", ctypes.c_void_p), ("db", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
+class RelposFwdArgs(ctypes.Structure):
+    _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("Nq", ctypes.c_int), ("Nk", ctypes.c_int),
+                ("E", ctypes.c_int), ("table_type", ctypes.c_int), ("table", ctypes.c_void_p),
+                ("edges", ctypes.c_void_p), ("pos_q", ctypes.c_void_p), ("pos_k", ctypes.c_void_p),
+                ("group_q", ctypes.c_void_p), ("group_k", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("base", Tensor4), ("bias", Tensor4)]
+
+
+class RelposBwdArgs(ctypes.Structure):
+    _fields_ = [("f", RelposFwdArgs), ("dbias", Tensor4), ("dtable", ctypes.c_void_p),
+                ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
+
+
 # The same two argument blocks as flat little-endian layouts (explicit padding), so a
 # call fills one buffer with a single pack instead of building a ctypes structure per
 # tensor; checked against the ctypes structures above at import.
 _FWD_PACK = struct.Struct("<4if4x" + "Q5q" * 3 + "Q4q" + "Q3q" + "Q5q" * 2 + "Q")
 _BWD_TAIL = struct.Struct("<" + "Q5q" * 4 + "Q4q" + "QQi4x")
 assert _FWD_PACK.size == ctypes.sizeof(FwdArgs) and FwdArgs.lse.offset == _FWD_PACK.size - 8
+# ... and those of the norm and the relative position bias
+_NORM_PACK = struct.Struct("<qQqQQQqQ" + "QqQqi4x" + "4if4x")
+_NORM_TAIL = struct.Struct("<QqQqQQQQ")
+_RELPOS_PACK = struct.Struct("<6i" + "6Q" + "2q" + "Q4q" * 2)
+_RELPOS_TAIL = struct.Struct("<Q4qQQQ")
+assert _NORM_PACK.size == ctypes.sizeof(NormFwdArgs) and NormFwdArgs.C.offset == _NORM_PACK.size - 24
+assert _NORM_PACK.size + _NORM_TAIL.size == ctypes.sizeof(NormBwdArgs)
+assert _RELPOS_PACK.size == ctypes.sizeof(RelposFwdArgs) and RelposFwdArgs.base.offset == _RELPOS_PACK.size - 80
+assert _RELPOS_PACK.size + _RELPOS_TAIL.size == ctypes.sizeof(RelposBwdArgs)
 assert _FWD_PACK.size + _BWD_TAIL.size == ctypes.sizeof(BwdArgs) and BwdArgs.dout.offset == _FWD_PACK.size
 
 
@@ -150,6 +193,19 @@ def load() -> ctypes.CDLL:
             lib.tri_attn_set_wait_limit_ns.restype = None
             lib.tri_attn_selftest_expire_wait.argtypes = [ctypes.c_void_p]
             lib.tri_attn_selftest_expire_wait.restype = ctypes.c_int
+            for n in ("tri_norm_fwd", "tri_norm_restore", "tri_norm_bwd", "tri_relpos_fwd", "tri_relpos_bwd"):
+                f = getattr(lib, n)
+                f.argtypes, f.restype = [ctypes.c_char_p, ctypes.c_void_p], ctypes.c_int
+            lib.tri_norm_bwd_workspace_bytes.argtypes = [ctypes.c_int64, ctypes.c_int]
+            lib.tri_norm_bwd_workspace_bytes.restype = ctypes.c_size_t
+            for n in ("tri_act8_pack", "tri_act8_unpack"):
+                getattr(lib, n).restype = ctypes.c_int
+            lib.tri_act8_pack.argtypes = [ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int,
+                                          Act8, ctypes.c_void_p]
+            lib.tri_act8_unpack.argtypes = [ctypes.c_int64, ctypes.c_int, Act8, ctypes.c_void_p, ctypes.c_int64,
+                                            ctypes.c_int, ctypes.c_void_p]
+            lib.tri_relpos_bwd_workspace_bytes.argtypes = [ctypes.c_int] * 6
+            lib.tri_relpos_bwd_workspace_bytes.restype = ctypes.c_size_t
             lib.tri_attn_abi_version.argtypes = []
             lib.tri_attn_abi_version.restype = ctypes.c_int
             _lib = lib
@@ -471,6 +527,245 @@ def tri_gate_bwd(z, o, wg, wo, dy, dz, d_o, dwg, dwo, workspace, stream=None) ->
     st = load().tri_gate_bwd(ctypes.byref(a), _stream_handle(stream))
     if st != TRI_ATTN_OK:
         raise TriAttnError(st, "tri_gate_bwd")
+
+
+# ---------------------------------------------------------------------------
+# layer norm, 8-bit activations, relative position bias
+#
+# The argument blocks are packed bytes (see _NORM_PACK, _RELPOS_PACK).  All
+# tensors of a call live on one CUDA device, which need not be the current one;
+# the call runs on the given stream, or that device's current stream.
+# ---------------------------------------------------------------------------
+
+def _run_on(where, tensors, stream, call):
+    """call(stream handle) with the device of `tensors` (None entries skipped) current; a
+    status other than 0 raises."""
+    import torch
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise TriAttnError(TRI_ATTN_ERR_UNSUPPORTED, f"{where}: every tensor must be on a CUDA device, got {t.device}")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise TriAttnError(TRI_ATTN_ERR_UNSUPPORTED, f"{where}: tensors on {dev} and {t.device}")
+    if stream is None:
+        stream = torch.cuda.current_stream(dev)
+    handle = stream if isinstance(stream, int) else stream.cuda_stream
+    if dev.index == torch.cuda.current_device():
+        st = call(handle)
+    else:
+        with torch.cuda.device(dev):
+            st = call(handle)
+    if st != TRI_ATTN_OK:
+        raise TriAttnError(st, where)
+
+
+def _float_type(t, name) -> int:
+    import torch
+    if t.dtype is torch.bfloat16:
+        return TRI_TYPE_BF16
+    if t.dtype is torch.float32:
+        return TRI_TYPE_F32
+    raise TriAttnError(TRI_ATTN_ERR_DTYPE, f"{name} must be bfloat16 or float32, got {t.dtype}")
+
+
+def _rows(t, name, shape=None):
+    """(R, C) of a 2-D tensor of rows with unit channel stride."""
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
+        raise TriAttnError(TRI_ATTN_ERR_SHAPE, f"{name} must be {list(shape) if shape else '[R, C]'}, got {list(t.shape)}")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise TriAttnError(TRI_ATTN_ERR_STRIDE, f"{name}: the channels must have stride 1")
+    return tuple(t.shape)
+
+
+def _dense(t, name, dtype, shape):
+    if t.dtype != dtype:
+        raise TriAttnError(TRI_ATTN_ERR_DTYPE, f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape or not t.is_contiguous():
+        raise TriAttnError(TRI_ATTN_ERR_SHAPE, f"{name} must be a contiguous {list(shape)} tensor, got {list(t.shape)}")
+
+
+def _affine(w, b, C):
+    """(w pointer, b pointer, type) of the norm's optional weight and bias."""
+    kind = TRI_TYPE_F32
+    for t, name in ((w, "weight"), (b, "bias")):
+        if t is not None:
+            kind = _float_type(t, name)
+            _dense(t, name, t.dtype, (C,))
+    if w is not None and b is not None and w.dtype != b.dtype:
+        raise TriAttnError(TRI_ATTN_ERR_DTYPE, f"weight and bias must have one dtype, got {w.dtype} and {b.dtype}")
+    return 0 if w is None else w.data_ptr(), 0 if b is None else b.data_ptr(), kind
+
+
+def _act8(codes, exps, kind, R, C):
+    import torch
+    want = {TRI_ACT8_INT8: torch.int8, TRI_ACT8_E4M3: torch.float8_e4m3fn}.get(kind)
+    if want is None:
+        raise TriAttnError(TRI_ATTN_ERR_UNSUPPORTED, f"kind must be TRI_ACT8_INT8 or TRI_ACT8_E4M3, got {kind}")
+    if codes.dtype != want or exps.dtype != torch.uint8:
+        raise TriAttnError(TRI_ATTN_ERR_DTYPE, f"codes must be {want} and exps uint8, got {codes.dtype} and {exps.dtype}")
+    _rows(codes, "codes", (R, C))
+    _rows(exps, "exps", (R, (C + 31) // 32))
+    return codes.data_ptr(), codes.stride(0), exps.data_ptr(), exps.stride(0), kind
+
+
+_NO_ACT8 = (0, 0, 0, 0, TRI_ACT8_NONE)
+
+
+def tri_norm_fwd(x, w, b, y, stats, codes=None, exps=None, kind: int = 0, eps: float = 1e-5, stream=None) -> None:
+    """y = (x - mean) * rstd * w + b over the channels of each row; x, y BF16 or FP32 [R, C]
+    (rows may be padded), w, b [C] or None, stats FP32 [2, R] written (means, rstds).  With
+    kind set, codes [R, C] and exps [R, ceil(C/32)] get x in 8 bits in the same pass."""
+    import torch
+    R, C = _rows(x, "x")
+    _rows(y, "y", (R, C))
+    _dense(stats, "stats", torch.float32, (2, R))
+    wp, bp, wt = _affine(w, b, C)
+    act = _act8(codes, exps, kind, R, C) if kind else _NO_ACT8
+    a = _NORM_PACK.pack(R, x.data_ptr(), x.stride(0), wp, bp, y.data_ptr(), y.stride(0), stats.data_ptr(), *act, C,
+                        _float_type(x, "x"), wt, _float_type(y, "y"), eps)
+    lib = load()
+    _run_on("tri_norm_fwd", (x, w, b, y, stats, codes, exps), stream, lambda s: lib.tri_norm_fwd(a, s))
+
+
+def tri_norm_restore(codes, exps, kind: int, stats, w, b, y, stream=None) -> None:
+    """The norm's output once more from what tri_norm_fwd kept: x in 8 bits and its stats."""
+    import torch
+    R, C = _rows(y, "y")
+    _dense(stats, "stats", torch.float32, (2, R))
+    wp, bp, wt = _affine(w, b, C)
+    a = _NORM_PACK.pack(R, 0, 0, wp, bp, y.data_ptr(), y.stride(0), stats.data_ptr(),
+                        *_act8(codes, exps, kind, R, C), C, 0, wt, _float_type(y, "y"), 0.0)
+    lib = load()
+    _run_on("tri_norm_restore", (codes, exps, stats, w, b, y), stream, lambda s: lib.tri_norm_restore(a, s))
+
+
+def tri_norm_bwd_workspace_bytes(R: int, C: int) -> int:
+    return int(load().tri_norm_bwd_workspace_bytes(R, C))
+
+
+def tri_norm_bwd(x, codes, exps, kind: int, stats, w, dy, dx, dw, db, workspace, stream=None) -> None:
+    """Gradients of the norm for the upstream dy [R, C].  x is the forward's input, or None
+    with kind, codes and exps set: its 8-bit form.  dx [R, C] has x's dtype (or None); dw, db
+    FP32 [C] (or both None); workspace a uint8 CUDA tensor of at least
+    tri_norm_bwd_workspace_bytes(R, C) bytes (None without dw and db)."""
+    import torch
+    R, C = _rows(dy, "dy")
+    _dense(stats, "stats", torch.float32, (2, R))
+    if (x is None) == (not kind):
+        raise TriAttnError(TRI_ATTN_ERR_NULL, "tri_norm_bwd: either x or its 8-bit form must be given")
+    if x is not None:
+        _rows(x, "x", (R, C))
+        xs, act, xt = (x.data_ptr(), x.stride(0)), _NO_ACT8, _float_type(x, "x")
+    else:
+        xs, act, xt = (0, 0), _act8(codes, exps, kind, R, C), TRI_TYPE_BF16
+    dxs = (0, 0)
+    if dx is not None:
+        _rows(dx, "dx", (R, C))
+        if x is not None and dx.dtype != x.dtype:
+            raise TriAttnError(TRI_ATTN_ERR_DTYPE, f"dx must be {x.dtype}, got {dx.dtype}")
+        dxs, xt = (dx.data_ptr(), dx.stride(0)), _float_type(dx, "dx")
+    if (dw is None) != (db is None):
+        raise TriAttnError(TRI_ATTN_ERR_NULL, "tri_norm_bwd: dw and db are given together or not at all")
+    for t, n in ((dw, "dw"), (db, "db")):
+        if t is not None:
+            _dense(t, n, torch.float32, (C,))
+    wp, _, wt = _affine(w, None, C)
+    ws = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    a = _NORM_PACK.pack(R, *xs, wp, 0, 0, 0, stats.data_ptr(), *act, C, xt, wt, _float_type(dy, "dy"), 0.0)
+    a += _NORM_TAIL.pack(dy.data_ptr(), dy.stride(0), *dxs, 0 if dw is None else dw.data_ptr(),
+                         0 if db is None else db.data_ptr(), *ws)
+    lib = load()
+    _run_on("tri_norm_bwd", (dy, x, codes, exps, stats, w, dx, dw, db, workspace), stream,
+            lambda s: lib.tri_norm_bwd(a, s))
+
+
+def tri_act8_pack(x, codes, exps, kind: int, stream=None) -> None:
+    """codes [R, C], exps [R, ceil(C/32)] = x [R, C] (BF16 or FP32) in 8 bits."""
+    R, C = _rows(x, "x")
+    act, xt = Act8(*_act8(codes, exps, kind, R, C)), _float_type(x, "x")
+    lib = load()
+    _run_on("tri_act8_pack", (x, codes, exps), stream,
+            lambda s: lib.tri_act8_pack(R, C, x.data_ptr(), x.stride(0), xt, act, s))
+
+
+def tri_act8_unpack(codes, exps, kind: int, x, stream=None) -> None:
+    """x [R, C] (BF16 or FP32) = the values that codes and exps stand for."""
+    R, C = _rows(x, "x")
+    act, xt = Act8(*_act8(codes, exps, kind, R, C)), _float_type(x, "x")
+    lib = load()
+    _run_on("tri_act8_unpack", (x, codes, exps), stream,
+            lambda s: lib.tri_act8_unpack(R, C, act, x.data_ptr(), x.stride(0), xt, s))
+
+
+def _relpos_index(pos_q, pos_k, group_q, group_k, edges):
+    import torch
+    if (group_q is None) != (group_k is None):
+        raise TriAttnError(TRI_ATTN_ERR_NULL, "group_q and group_k are given together or not at all")
+    for t, n, d in ((pos_q, "pos_q", 2), (pos_k, "pos_k", 2), (group_q, "group_q", 2), (group_k, "group_k", 2),
+                    (edges, "edges", 1)):
+        if t is None:
+            continue
+        _check_tensor(t, n, torch.int32, d)
+        if t.shape[-1] > 1 and t.stride(-1) != 1:
+            raise TriAttnError(TRI_ATTN_ERR_STRIDE, f"{n} must have unit inner stride")
+    for g, t, n in ((group_q, pos_q, "group_q"), (group_k, pos_k, "group_k")):
+        if g is not None and (g.shape != t.shape or (t.shape[0] > 1 and g.stride(0) != t.stride(0))):
+            raise TriAttnError(TRI_ATTN_ERR_SHAPE, f"{n} must be laid out as its positions are")
+    if pos_q.shape[0] != pos_k.shape[0]:
+        raise TriAttnError(TRI_ATTN_ERR_SHAPE, "pos_q and pos_k must have one batch size")
+    ptr = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
+    return (ptr(edges), ptr(pos_q), ptr(pos_k), ptr(group_q), ptr(group_k), pos_q.stride(0), pos_k.stride(0))
+
+
+def _relpos_bias(t, name, B, H, Nq, Nk):
+    if t is None:
+        return 0, 0, 0, 0, 0
+    v = _v4(t, name)
+    if tuple(t.shape) != (B, H, Nq, Nk):
+        raise TriAttnError(TRI_ATTN_ERR_SHAPE, f"{name} must be {[B, H, Nq, Nk]}, got {list(t.shape)}")
+    # the stride of a dimension of one element means nothing: any multiple of 8 will do
+    return v[0], *(s if n > 1 else 0 for s, n in zip(v[1:4], t.shape)), v[4] if Nk > 1 else 1
+
+
+def tri_relpos_fwd(table, edges, pos_q, pos_k, group_q, group_k, base, bias, stream=None) -> None:
+    """bias[b,h,i,j] = table[bucket(pos_k[b,j] - pos_q[b,i]), h] (+ base); bias, base BF16
+    [B,H,Nq,Nk] (base may be None), table [buckets, H], positions and groups int32 [B, N]."""
+    if table.dim() != 2 or not table.is_contiguous():
+        raise TriAttnError(TRI_ATTN_ERR_SHAPE, "table must be a contiguous [buckets, H] tensor")
+    idx = _relpos_index(pos_q, pos_k, group_q, group_k, edges)
+    (nb, H), (B, Nq), Nk, E = table.shape, pos_q.shape, pos_k.shape[1], edges.shape[0]
+    if nb != E + 1 + (group_q is not None):
+        raise TriAttnError(TRI_ATTN_ERR_SHAPE, f"table must have {E + 1 + (group_q is not None)} rows, got {nb}")
+    a = _RELPOS_PACK.pack(B, H, Nq, Nk, E, _float_type(table, "table"), table.data_ptr(), *idx,
+                          *_relpos_bias(base, "base", B, H, Nq, Nk), *_relpos_bias(bias, "bias", B, H, Nq, Nk))
+    lib = load()
+    _run_on("tri_relpos_fwd", (table, edges, pos_q, pos_k, group_q, group_k, base, bias), stream,
+            lambda s: lib.tri_relpos_fwd(a, s))
+
+
+def tri_relpos_bwd_workspace_bytes(B: int, H: int, Nq: int, Nk: int, E: int, groups: bool) -> int:
+    return int(load().tri_relpos_bwd_workspace_bytes(B, H, Nq, Nk, E, int(groups)))
+
+
+def tri_relpos_bwd(dbias, edges, pos_q, pos_k, group_q, group_k, dtable, workspace, stream=None) -> None:
+    """dtable [buckets, H] (FP32) = the sums of dbias (BF16 [B,H,Nq,Nk]) by bucket; workspace a
+    uint8 CUDA tensor of at least tri_relpos_bwd_workspace_bytes(...) bytes."""
+    import torch
+    idx = _relpos_index(pos_q, pos_k, group_q, group_k, edges)
+    if dbias.dim() != 4:
+        raise TriAttnError(TRI_ATTN_ERR_SHAPE, "dbias must be [B, H, Nq, Nk]")
+    (B, Nq), Nk, E, H = pos_q.shape, pos_k.shape[1], edges.shape[0], dbias.shape[1]
+    _dense(dtable, "dtable", torch.float32, (E + 1 + (group_q is not None), H))
+    a = _RELPOS_PACK.pack(B, H, Nq, Nk, E, 0, 0, *idx, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
+    a += _RELPOS_TAIL.pack(*_relpos_bias(dbias, "dbias", B, H, Nq, Nk), dtable.data_ptr(), workspace.data_ptr(),
+                           workspace.numel() * workspace.element_size())
+    lib = load()
+    _run_on("tri_relpos_bwd", (dbias, edges, pos_q, pos_k, group_q, group_k, dtable, workspace), stream,
+            lambda s: lib.tri_relpos_bwd(a, s))
 
 
 def tri_attn_device_error(clear: bool = True):

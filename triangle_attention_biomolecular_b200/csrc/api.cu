@@ -16,6 +16,7 @@
 #include <cstdlib>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 
 #include "../../include/tri_attn.h"
 #include "sm100.cuh"
@@ -24,6 +25,8 @@
 #include "dbias.cuh"
 #include "tri_mul.cuh"
 #include "tri_gate.cuh"
+#include "tri_norm.cuh"
+#include "tri_relpos.cuh"
 
 namespace {
 
@@ -139,6 +142,8 @@ tri_attn_status ensure_device() {
                                tri::TriGateLayout::SMEM) == cudaSuccess;
     ok &= cudaFuncSetAttribute(tri::tri_gate_bwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                tri::TriGateBwdLayout::SMEM) == cudaSuccess;
+    ok &= cudaFuncSetAttribute(tri::tri_relpos_bwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024) ==
+          cudaSuccess;
     if (!ok || !encoder()) {
         cudaGetLastError();
         return TRI_ATTN_ERR_CUDA;
@@ -689,3 +694,5 @@ extern "C" tri_attn_status tri_attn_selftest_expire_wait(tri_attn_stream_t strea
     tri::selftest_expire_kernel<<<1, 32, 0, reinterpret_cast<cudaStream_t>(stream)>>>(g_wait_limit_ns.load());
     return cudaGetLastError() == cudaSuccess ? TRI_ATTN_OK : TRI_ATTN_ERR_CUDA;
 }
+
+#include "pair_ops.cuh"  // the exported entry points of the norm, the 8-bit activation and the position bias

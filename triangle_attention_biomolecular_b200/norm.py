@@ -1,0 +1,216 @@
+"""Layer norm of pair rows and the 8-bit activation checkpoint.
+
+``layer_norm(x, weight, bias)`` normalises the last dimension of a BF16 or FP32
+tensor and is differentiable in all three.  With ``checkpoint="int8"`` or
+``"e4m3"`` the forward keeps x in 8 bits (1.03 bytes a value in place of 2 or 4)
+and the backward reads that form.  ``norm_linear`` puts the projection that
+follows into the same step, so that neither x nor the norm's output is kept:
+the backward restores the output from the 8-bit x and the row statistics.
+
+The 8-bit form (:class:`Act8`): 32 neighbouring channels share a power-of-two
+scale, the least under which the block's largest magnitude fits the code range
+(127 for int8, 448 for e4m3).  Restoring to BF16 adds no rounding.  A block
+that holds an infinity or a NaN is restored as NaNs.
+
+These functions run on the current stream of their tensors' device.  To capture
+a training step into a CUDA graph, run the whole step (forward and backward)
+once on a side stream first, and capture it with no autograd graph of an
+earlier eager step on the same leaves still alive: autograd ties the
+accumulation of a leaf's gradient to the stream of the oldest live graph, as
+for any other operator.
+"""
+from __future__ import annotations
+
+from typing import NamedTuple, Optional
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import _binding as B
+
+_KINDS = {"int8": (B.TRI_ACT8_INT8, torch.int8), "e4m3": (B.TRI_ACT8_E4M3, torch.float8_e4m3fn)}
+
+
+class Act8(NamedTuple):
+    """An activation in 8 bits: codes of x's shape, exponent bytes [..., ceil(C/32)] and the
+    dtype x had."""
+    codes: torch.Tensor
+    exps: torch.Tensor
+    dtype: torch.dtype
+
+    @property
+    def kind(self) -> int:
+        return B.TRI_ACT8_INT8 if self.codes.dtype == torch.int8 else B.TRI_ACT8_E4M3
+
+    @property
+    def nbytes(self) -> int:
+        return self.codes.numel() + self.exps.numel()
+
+
+def _kind(name: str):
+    try:
+        return _KINDS[name]
+    except (KeyError, TypeError):
+        raise ValueError(f"checkpoint kind must be 'int8' or 'e4m3', got {name!r}") from None
+
+
+def _rows(x: torch.Tensor) -> torch.Tensor:
+    """x as [R, C] rows with unit channel stride, without a copy where its strides allow it."""
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise B.TriAttnError(B.TRI_ATTN_ERR_SHAPE, f"a tensor of rows of at least one channel is needed, got {list(x.shape)}")
+    C = x.shape[-1]
+    R = x.numel() // C
+    if x.is_contiguous():
+        return x.view(R, C)
+    if x.stride(-1) == 1:
+        try:
+            return x.view(R, C)
+        except RuntimeError:
+            pass
+    return x.contiguous().view(R, C)
+
+
+def _param(p: Optional[torch.Tensor]):
+    return None if p is None else p.contiguous()
+
+
+def _empty8(x: torch.Tensor, kind: str):
+    _, dt = _kind(kind)
+    codes = torch.empty(x.shape, dtype=dt, device=x.device)
+    exps = torch.empty((*x.shape[:-1], (x.shape[-1] + 31) // 32), dtype=torch.uint8, device=x.device)
+    return Act8(codes, exps, x.dtype)
+
+
+def act8_pack(x: torch.Tensor, kind: str = "int8") -> Act8:
+    """x (BF16 or FP32, [..., C]) in 8 bits."""
+    x2 = _rows(x)
+    a = _empty8(x, kind)
+    B.tri_act8_pack(x2, _rows(a.codes), _rows(a.exps), a.kind)
+    return a
+
+
+def act8_unpack(a: Act8, dtype: Optional[torch.dtype] = None) -> torch.Tensor:
+    """The values a stands for, in ``dtype`` (default: the dtype that was packed)."""
+    x = torch.empty(a.codes.shape, dtype=dtype or a.dtype, device=a.codes.device)
+    B.tri_act8_unpack(_rows(a.codes), _rows(a.exps), a.kind, _rows(x))
+    return x
+
+
+def norm_forward(x, weight=None, bias=None, eps: float = 1e-5, out_dtype: Optional[torch.dtype] = None,
+                 checkpoint: Optional[str] = None):
+    """Returns (y, stats, kept): y of x's shape in ``out_dtype`` (default: x's dtype), stats FP32
+    [2, rows] (means, reciprocal standard deviations), and kept, x as an :class:`Act8` written
+    in the same pass (None without ``checkpoint``)."""
+    x2 = _rows(x)
+    y = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
+    stats = torch.empty((2, x2.shape[0]), dtype=torch.float32, device=x.device)
+    weight, bias = _param(weight), _param(bias)
+    if checkpoint is None:
+        B.tri_norm_fwd(x2, weight, bias, _rows(y), stats, eps=eps)
+        return y, stats, None
+    a = _empty8(x, checkpoint)
+    B.tri_norm_fwd(x2, weight, bias, _rows(y), stats, _rows(a.codes), _rows(a.exps), a.kind, eps)
+    return y, stats, a
+
+
+def norm_restore(kept: Act8, stats, weight=None, bias=None, out_dtype: Optional[torch.dtype] = None):
+    """The norm's output from the 8-bit x and the statistics of :func:`norm_forward`."""
+    y = torch.empty(kept.codes.shape, dtype=out_dtype or kept.dtype, device=kept.codes.device)
+    B.tri_norm_restore(_rows(kept.codes), _rows(kept.exps), kept.kind, stats, _param(weight), _param(bias), _rows(y))
+    return y
+
+
+def norm_backward(x, stats, dy, weight=None, need_dx: bool = True, need_dw: Optional[bool] = None):
+    """Returns (dx, dweight, dbias) for the upstream gradient dy; ``x`` is the forward's input or
+    the :class:`Act8` it kept.  dx has x's dtype; dweight and dbias are FP32 [C] (None unless
+    ``need_dw``, by default when there is a weight)."""
+    dy2 = _rows(dy)
+    R, C = dy2.shape
+    kept = isinstance(x, Act8)
+    x2, codes, exps, kind = (None, _rows(x.codes), _rows(x.exps), x.kind) if kept else (_rows(x), None, None, 0)
+    dx = dw = db = ws = None
+    if need_dx:
+        dx = torch.empty(dy.shape, dtype=x.dtype, device=dy.device)
+    if weight is not None if need_dw is None else need_dw:
+        grads = torch.empty((2, C), dtype=torch.float32, device=dy.device)
+        dw, db = grads[0], grads[1]
+        ws = torch.empty(B.tri_norm_bwd_workspace_bytes(R, C), dtype=torch.uint8, device=dy.device)
+    B.tri_norm_bwd(x2, codes, exps, kind, stats, _param(weight), dy2, None if dx is None else _rows(dx), dw, db, ws)
+    return dx, dw, db
+
+
+def _save(ctx, x, kept, stats, *more):
+    """Keeps x, or its 8-bit form in place of it."""
+    ctx.x_dtype = None if kept is None else kept.dtype
+    first = (x,) if kept is None else (kept.codes, kept.exps)
+    ctx.save_for_backward(*first, stats, *more)
+
+
+def _saved(ctx):
+    s = ctx.saved_tensors
+    if ctx.x_dtype is None:
+        return s
+    return (Act8(s[0], s[1], ctx.x_dtype), *s[2:])
+
+
+def _like(g, p):
+    return None if p is None else g.to(p.dtype)
+
+
+class LayerNormFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, eps, out_dtype, checkpoint):
+        y, stats, kept = norm_forward(x, weight, bias, eps, out_dtype, checkpoint)
+        _save(ctx, x, kept, stats, weight, bias)
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, stats, weight, bias = _saved(ctx)
+        need = ctx.needs_input_grad
+        dx, dw, db = norm_backward(x, stats, dy, weight, need[0], need[1] or need[2])
+        return dx, _like(dw, weight) if need[1] else None, _like(db, bias) if need[2] else None, None, None, None
+
+
+def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out_dtype: Optional[torch.dtype] = None,
+               checkpoint: Optional[str] = None):
+    """Differentiable layer norm over the last dimension (BF16 or FP32 in, ``out_dtype`` out).
+    ``checkpoint`` "int8" or "e4m3" keeps x in 8 bits for the backward."""
+    if checkpoint is not None:
+        _kind(checkpoint)
+    return LayerNormFunction.apply(x, weight, bias, eps, out_dtype, checkpoint)
+
+
+class NormLinearFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, proj, eps, checkpoint):
+        y, stats, kept = norm_forward(x, weight, bias, eps, proj.dtype, checkpoint)
+        _save(ctx, x, kept, stats, weight, bias, proj)
+        ctx.eps = eps
+        return torch.matmul(y, proj.t())
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g):
+        x, stats, weight, bias, proj = _saved(ctx)
+        need = ctx.needs_input_grad
+        dx = dw = db = dproj = None
+        if need[3]:
+            if isinstance(x, Act8):
+                y = norm_restore(x, stats, weight, bias, proj.dtype)
+            else:
+                y = norm_forward(x, weight, bias, ctx.eps, proj.dtype)[0]
+            dproj = torch.matmul(g.reshape(-1, g.shape[-1]).t(), _rows(y))
+        if need[0] or need[1] or need[2]:
+            dx, dw, db = norm_backward(x, stats, torch.matmul(g, proj), weight, need[0], need[1] or need[2])
+        return (dx, _like(dw, weight) if need[1] else None, _like(db, bias) if need[2] else None, dproj, None, None)
+
+
+def norm_linear(x, weight, bias, proj, eps: float = 1e-5, checkpoint: Optional[str] = "int8"):
+    """layer_norm(x) @ proj.T, differentiable in x, weight, bias and proj ([out, C], BF16 or FP32;
+    it sets the dtype of the norm's output and of the result).  Between the passes only x is
+    kept, in 8 bits unless ``checkpoint`` is None; the norm's output is computed again."""
+    if checkpoint is not None:
+        _kind(checkpoint)
+    return NormLinearFunction.apply(x, weight, bias, proj, eps, checkpoint)

@@ -1,0 +1,133 @@
+"""Learned relative position bias for the attention's bias input.
+
+A distance ``pos_k[b, j] - pos_q[b, i]`` falls into the bucket counted by the
+edges that are not above it (``edges`` ascending, int32, above -2**31), and the
+bias is that row of a learned table; with groups (chains, segments) a pair of
+different groups takes the table's last row.  :func:`relpos_edges_clipped` and
+:func:`relpos_edges_log` build the two usual sets of edges.
+
+``relative_position_bias`` returns BF16 [B, H, Nq, Nk] in the padded layout that
+``triangle_attention`` reads, is differentiable in the table and in ``base`` (a
+bias to add to, such as a projected pair bias), and gives the table's gradient
+in one pass over the bias's, with no atomics: repeated runs are bitwise equal.
+"""
+from __future__ import annotations
+
+from typing import Optional
+
+import torch
+from torch.autograd.function import once_differentiable
+
+from . import _binding as B
+
+
+def relpos_edges_clipped(r: int, device="cuda") -> torch.Tensor:
+    """Edges of 2 r + 1 buckets: each distance from -r to r its own, farther ones with the ends."""
+    if not 1 <= r <= 255:
+        raise B.TriAttnError(B.TRI_ATTN_ERR_SHAPE, f"r must be from 1 to 255, got {r}")
+    return torch.arange(1 - r, r + 1, dtype=torch.int32, device=device)
+
+
+def relpos_edges_log(per_side: int, max_distance: int, device="cuda") -> torch.Tensor:
+    """Edges of 2 * per_side + 1 buckets: distance 0, and per_side buckets to either side, the
+    first half of them one distance each, the others growing geometrically up to the last,
+    which starts at max_distance."""
+    if not 1 <= per_side <= 255 or not per_side <= max_distance < 2 ** 31:
+        raise B.TriAttnError(B.TRI_ATTN_ERR_SHAPE,
+                             f"1 <= per_side <= 255 and per_side <= max_distance < 2**31 are needed, got {per_side}, {max_distance}")
+    exact = (per_side + 1) // 2
+    steps = per_side - exact
+    up = list(range(1, exact + 1))
+    for k in range(1, steps + 1):
+        # least n with (n / exact)^steps >= (max_distance / exact)^k, in whole numbers
+        n = int(exact * (max_distance / exact) ** (k / steps))
+        bound = exact ** (steps - k) * max_distance ** k
+        while n ** steps >= bound:
+            n -= 1
+        while n ** steps < bound:
+            n += 1
+        up.append(max(n, up[-1] + 1))
+    return torch.tensor([1 - u for u in reversed(up)] + up, dtype=torch.int32, device=device)
+
+
+def _layout(t: torch.Tensor) -> torch.Tensor:
+    """t itself if the C ABI accepts its layout (unit inner stride, the others non-negative
+    multiples of 8, 16-byte aligned data), else a copy with rows padded to a multiple of 8."""
+    ok = (t.shape[3] == 1 or t.stride(3) == 1) and t.data_ptr() % 16 == 0
+    if ok and all(n == 1 or (s >= 0 and s % 8 == 0) for n, s in zip(t.shape[:3], t.stride()[:3])):
+        return t
+    return _padded(t.shape, t.device).copy_(t)
+
+
+def _padded(shape, device) -> torch.Tensor:
+    *lead, n = shape
+    return torch.empty((*lead, (n + 7) // 8 * 8), dtype=torch.bfloat16, device=device)[..., :n]
+
+
+def _index(pos_q, pos_k, group_q, group_k, like=None):
+    """Positions and groups as int32 [B, N], one batch size (that of ``like`` where all are shared),
+    groups laid out as the positions."""
+    ts = [pos_q, pos_k, group_q, group_k]
+    for t in ts:
+        if t is not None and (t.dtype != torch.int32 or not 1 <= t.dim() <= 2):
+            raise B.TriAttnError(B.TRI_ATTN_ERR_DTYPE, f"positions and groups are int32 [N] or [B, N], got {t.dtype} {list(t.shape)}")
+    ts = [t if t is None or t.dim() == 2 else t[None] for t in ts]
+    n = max([t.shape[0] for t in ts if t is not None] + ([] if like is None else [like.shape[0]]))
+    if any(t is not None and t.shape[0] not in (1, n) for t in ts):
+        raise B.TriAttnError(B.TRI_ATTN_ERR_SHAPE, "positions and groups of different batch sizes")
+    out = []
+    for p, g in ((ts[0], ts[2]), (ts[1], ts[3])):
+        p = p.expand(n, -1)
+        if g is not None:
+            g = g.expand(n, -1)
+            if g.stride() != p.stride():
+                p, g = p.contiguous(), g.contiguous()
+        if p.stride(1) != 1:
+            p, g = p.contiguous(), None if g is None else g.contiguous()
+        out.append((p, g))
+    return out[0][0], out[1][0], out[0][1], out[1][1]
+
+
+def relpos_forward(table, edges, pos_q, pos_k, group_q=None, group_k=None, base=None):
+    """The bias, BF16 [B, H, Nq, Nk] with rows padded to a multiple of 8 elements.  table BF16 or
+    FP32 [buckets, H]; positions and groups int32 [N] or [B, N]; base BF16 [B, H, Nq, Nk]."""
+    q, k, gq, gk = _index(pos_q, pos_k, group_q, group_k, base)
+    bias = _padded((q.shape[0], table.shape[1], q.shape[1], k.shape[1]), table.device)
+    B.tri_relpos_fwd(table.contiguous(), edges, q, k, gq, gk, None if base is None else _layout(base), bias)
+    return bias
+
+
+def relpos_backward(dbias, edges, pos_q, pos_k, group_q=None, group_k=None):
+    """The table's gradient, FP32 [buckets, H], for the bias's gradient (BF16 [B, H, Nq, Nk])."""
+    q, k, gq, gk = _index(pos_q, pos_k, group_q, group_k, dbias)
+    E, H = edges.shape[0], dbias.shape[1]
+    dtable = torch.empty((E + 1 + (gq is not None), H), dtype=torch.float32, device=dbias.device)
+    need = B.tri_relpos_bwd_workspace_bytes(q.shape[0], H, q.shape[1], k.shape[1], E, gq is not None)
+    ws = torch.empty(need, dtype=torch.uint8, device=dbias.device)
+    B.tri_relpos_bwd(_layout(dbias), edges, q, k, gq, gk, dtable, ws)
+    return dtable
+
+
+class RelativePositionBiasFunction(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, table, base, edges, pos_q, pos_k, group_q, group_k):
+        ctx.save_for_backward(edges, pos_q, pos_k, group_q, group_k)
+        ctx.table_dtype = table.dtype
+        return relpos_forward(table, edges, pos_q, pos_k, group_q, group_k, base)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, g):
+        dtable = None
+        if ctx.needs_input_grad[0]:
+            dtable = relpos_backward(g, *ctx.saved_tensors).to(ctx.table_dtype)
+        return dtable, g if ctx.needs_input_grad[1] else None, None, None, None, None, None
+
+
+def relative_position_bias(table, edges, pos_q, pos_k=None, group_q=None, group_k=None,
+                           base: Optional[torch.Tensor] = None):
+    """Differentiable relative position bias (see :func:`relpos_forward`); without ``pos_k`` the
+    keys have the queries' positions and groups."""
+    if pos_k is None:
+        pos_k, group_k = pos_q, group_q
+    return RelativePositionBiasFunction.apply(table, base, edges, pos_q, pos_k, group_q, group_k)
