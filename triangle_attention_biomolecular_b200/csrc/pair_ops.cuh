@@ -227,27 +227,36 @@ void relpos_params(RelposParams& p, const tri_relpos_fwd_args& a) {
 
 // launch shape of the backward: a function of the sizes alone
 struct RelposBwdShape {
-    int heads, head_blocks, warps, rows_per_task, row_tasks;
+    int heads, head_blocks, warps, row_tasks;
     unsigned grid;
     size_t smem;
 };
 RelposBwdShape relpos_bwd_shape(int B, int H, int Nq, int Nk, int nb) {
     RelposBwdShape s{};
-    s.heads = 1;
-    while (s.heads < H && s.heads < 32) s.heads *= 2;
+    // a warp's lanes: 8 chunks of four heads, 16 of two or 32 of one, or fewer chunks where there
+    // are no more; of these the one that leaves the fewest lanes without work, the narrowest first
+    // (the fewer keys a warp spans, the fewer of its rows have one of them near the diagonal)
+    const int chunks = (Nk + 7) / 8;
+    int64_t fewest = INT64_MAX;
+    for (int heads = 32; heads >= 1; heads /= 2) {
+        const int side = 32 / heads;
+        const int64_t lanes = static_cast<int64_t>((chunks + side - 1) / side) * side * ((H + heads - 1) / heads * heads);
+        if (lanes < fewest && (heads <= 4 || side >= chunks)) {
+            fewest = lanes;
+            s.heads = heads;
+        }
+    }
     s.head_blocks = (H + s.heads - 1) / s.heads;
-    const int S = 32 / s.heads, chunks = (Nk + 7) / 8;
+    const int S = 32 / s.heads;
     const int64_t tiles = static_cast<int64_t>(B) * ((chunks + S - 1) / S);
     s.warps = tri::kRelBwdWarps;
     while (s.warps > 1 && tri::relpos_bwd_smem(nb, s.warps) > 200 * 1024) --s.warps;
     s.smem = tri::relpos_bwd_smem(nb, s.warps);
-    const int64_t want = std::max<int64_t>(1, 148 * 16 / (tiles * s.head_blocks));
-    const int64_t most = std::max(1, Nq / 4);
-    s.row_tasks = static_cast<int>(std::min(want, most));
-    s.rows_per_task = (Nq + s.row_tasks - 1) / s.row_tasks;
-    s.row_tasks = (Nq + s.rows_per_task - 1) / s.rows_per_task;
+    // as many tasks as warps run at once, each with at least one batch of rows
+    const int64_t want = std::max<int64_t>(1, 148 * 20 / (tiles * s.head_blocks));
+    s.row_tasks = static_cast<int>(std::min<int64_t>(want, (Nq + tri::kRelRows - 1) / tri::kRelRows));
     const int64_t tasks = tiles * s.row_tasks;
-    s.grid = static_cast<unsigned>(std::min<int64_t>((tasks + s.warps - 1) / s.warps, 148 * 4));
+    s.grid = static_cast<unsigned>(std::min<int64_t>((tasks + s.warps - 1) / s.warps, 148 * 5));
     return s;
 }
 
@@ -390,7 +399,6 @@ tri_attn_status tri_relpos_bwd(const tri_relpos_bwd_args* a, tri_attn_stream_t s
     relpos_params(p, f);
     const RelposBwdShape s = relpos_bwd_shape(f.B, f.H, f.Nq, f.Nk, p.nb);
     p.heads = s.heads;
-    p.rows_per_task = s.rows_per_task;
     p.row_tasks = s.row_tasks;
     p.partial = static_cast<float*>(a->workspace);
     p.dbias = static_cast<const __nv_bfloat16*>(a->dbias.ptr);

@@ -14,15 +14,14 @@
 namespace tri {
 
 constexpr int kRelMaxEdges = 510;
-// distances between the first and the last edge that get a table of their
-// buckets in shared memory; wider edges are searched
+// distances whose buckets are tabulated in shared memory
 constexpr int kRelLut = 2048;
 
 struct RelposParams {
     int B, H, Nq, Nk, E;
     int nb;        // buckets, the one for different groups included
     int chunks;    // ceil(Nk / 8)
-    int heads;     // heads per block (grid.y chunks of them)
+    int heads;     // heads per block (grid.y chunks of them); backward: per warp
     const void* table;
     int table_bf16;
     const int32_t* edges;
@@ -34,22 +33,24 @@ struct RelposParams {
     int64_t os[3];
     const __nv_bfloat16* dbias;
     int64_t ds[3];
-    int rows_per_task, row_tasks;  // backward: rows a warp walks, and tasks per column tile
+    int row_tasks;                 // backward: warps that share the rows of a column tile
     float* partial;                // backward: [gridDim.x][nb][H]
 };
 
 // Buckets of distances.  edges and lut are shared memory, filled by init (every
-// thread of the block; a barrier follows).
+// thread of the block; a barrier follows).  Distances from lo to lo + kRelLut - 1
+// are looked up: all there are (others are clamped to the ends) when the edges
+// lie that close together, else the kRelLut around 0, and those outside are
+// searched.
 struct RelposBuckets {
     const int32_t* edges;
     const uint16_t* lut;
-    int E, lo, hi;
-    bool table;
+    int E, lo, size, dmin, dmax;
 
     // number of edges <= d
     __device__ __forceinline__ int search(int d) const {
         int n = 0;
-#pragma unroll
+#pragma unroll 1
         for (int s = 256; s > 0; s >>= 1)
             if (n + s <= E && edges[n + s - 1] <= d) n += s;
         return n;
@@ -60,24 +61,35 @@ struct RelposBuckets {
         edges = sh_edges;
         lut = sh_lut;
         E = p.E;
-        lo = sh_edges[0];
-        hi = sh_edges[E - 1];
-        const int64_t span = static_cast<int64_t>(hi) - lo + 2;
-        table = span >= 2 && span <= kRelLut && lo != INT32_MIN;
-        if (table) {
-            lo -= 1;
-            for (int x = threadIdx.x; x < static_cast<int>(span); x += blockDim.x)
-                sh_lut[x] = static_cast<uint16_t>(search(lo + x));
+        const int first = sh_edges[0], last = sh_edges[E - 1];
+        const int64_t span = static_cast<int64_t>(last) - first + 2;
+        if (span >= 2 && span <= kRelLut && first != INT32_MIN) {
+            lo = dmin = first - 1;
+            dmax = last;
+            size = static_cast<int>(span);
+        } else {
+            lo = -kRelLut / 2;
+            size = kRelLut;
+            dmin = INT32_MIN;
+            dmax = INT32_MAX;
         }
+        for (int x = threadIdx.x; x < size; x += blockDim.x) sh_lut[x] = static_cast<uint16_t>(search(lo + x));
         __syncthreads();
     }
-    __device__ __forceinline__ int operator()(int pk, int pq) const {
-        // saturating: a difference past 32 bits lies beyond every edge (or, at the
-        // lowest value, is compared as that value)
+    // pk - pq, saturating: a difference past 32 bits lies beyond every edge
+    static __device__ __forceinline__ int distance(int pk, int pq) {
         int d;
         asm("sub.sat.s32 %0, %1, %2;" : "=r"(d) : "r"(pk), "r"(pq));
-        return table ? lut[min(max(d, lo), hi) - lo] : search(d);
+        return d;
     }
+    __device__ __forceinline__ int of(int d) const {
+        d = min(max(d, dmin), dmax);
+        const uint32_t x = static_cast<uint32_t>(d) - static_cast<uint32_t>(lo);
+        return x < static_cast<uint32_t>(size) ? lut[x] : search(d);
+    }
+    // the distances of bucket k are least(k) <= d <= most(k)
+    __device__ __forceinline__ int least(int k) const { return k > 0 ? edges[k - 1] : INT32_MIN; }
+    __device__ __forceinline__ int most(int k) const { return k < E ? edges[k] - 1 : INT32_MAX; }
 };
 
 constexpr int kRelThreads = 256;
@@ -122,13 +134,29 @@ __global__ void __launch_bounds__(kRelThreads) tri_relpos_fwd_kernel(const __gri
         const int gq = p.grp_q ? p.grp_q[b * p.qs + i] : 0;
         const int32_t* pk = p.pos_k + b * p.ks + j0;
         const int32_t* gk = p.grp_k ? p.grp_k + b * p.ks + j0 : nullptr;
-        int at[8];
+        // a chunk whose nearest and farthest key lie in one bucket needs no other look
+        int key[8], at[8];
+        int pmin = INT32_MAX, pmax = INT32_MIN;
+        bool same = true, apart = true;  // all keys of the query's group; none
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
             const int xx = min(x, nj - 1);
-            int k = bucket(pk[xx], pq);
-            if (gk && gk[xx] != gq) k = p.E + 1;
-            at[x] = k * pitch;
+            key[x] = pk[xx];
+            pmin = min(pmin, key[x]);
+            pmax = max(pmax, key[x]);
+            at[x] = gk && gk[xx] != gq;
+            same &= !at[x];
+            apart &= at[x] != 0;
+        }
+        const int first = apart ? p.E + 1 : bucket.of(RelposBuckets::distance(pmin, pq));
+        const bool one = apart || (same && first == bucket.of(RelposBuckets::distance(pmax, pq)));
+        if (one) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x) at[x] = first * pitch;
+        } else {
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+                at[x] = (at[x] ? p.E + 1 : bucket.of(RelposBuckets::distance(key[x], pq))) * pitch;
         }
         __nv_bfloat16* out = p.bias + b * p.os[0] + h0 * p.os[1] + i * p.os[2] + j0;
         const __nv_bfloat16* in = BASE ? p.base + b * p.bs[0] + h0 * p.bs[1] + i * p.bs[2] + j0 : nullptr;
@@ -168,35 +196,97 @@ __global__ void __launch_bounds__(kRelThreads) tri_relpos_fwd_kernel(const __gri
     }
 }
 
-// Backward.  A warp takes Hc heads (H rounded up to a power of two, at most 32)
-// by S = 32 / Hc chunks of eight keys and walks down the rows i of its task; a
-// lane keeps to one head and one chunk of keys.  Each lane owns a column of the
-// warp's sums in shared memory, [bucket][lane]: no two lanes ever meet in a
-// word (nor, 32 lanes to 32 banks, in a bank), so there are no atomics and
-// every sum has one order.  Most chunks lie in one bucket as a whole (beyond
-// the clipping distance, or in another chain): the bucket of the smallest and
-// the largest position of the chunk tell, and the eight values then go into a
-// register that is put down only when the bucket changes.
+// Backward.  A warp takes S chunks of eight keys by 32 / S heads and walks down
+// rows i; a lane keeps to one head and one chunk.  Each lane owns a column of the
+// warp's sums in shared memory, [bucket][lane]: no two lanes ever meet in a word
+// (nor, 32 lanes to 32 banks, in a bank), so there are no atomics and every sum
+// has one order.
+//
+// Most chunks lie in one bucket as a whole (beyond the clipping distance, or in
+// another group) or across one edge.  A lane therefore holds two neighbouring
+// buckets in hand, each with a sum in a register, and the bounds that tell with two
+// comparisons that a chunk lies within them; they are put down into the column
+// when a chunk does not.  Rows are taken kRelRows at a time, so that their loads
+// are in flight together; the few rows that need more than the registers are read
+// again afterwards (from the cache) by one compact loop: unrolled into the walk,
+// that code did not fit the instruction cache.  A task's batches of rows lie a
+// whole round of tasks apart, since the rows near the diagonal cost the most.
 constexpr int kRelBwdWarps = 4;
+constexpr int kRelRows = 8;
 
 __host__ constexpr size_t relpos_bwd_smem(int nb, int warps) {
     return static_cast<size_t>(warps) * nb * 32 * 4 + 512 * 4 + kRelLut * 2;
 }
 
-__global__ void __launch_bounds__(kRelBwdWarps * 32) tri_relpos_bwd_kernel(const __grid_constant__ RelposParams p) {
+// the two buckets a lane has in hand: first and first + 1
+struct RelposPair {
+    int first, E;
+    int least, edge, most;  // distances least .. edge - 1 and edge .. most
+    float sum[2];
+    __device__ __forceinline__ void take(const RelposBuckets& bucket, int k) {
+        first = k;
+        E = bucket.E;
+        least = bucket.least(k);
+        edge = k < bucket.E ? bucket.edges[k] : INT32_MAX;
+        most = bucket.most(min(k + 1, bucket.E));
+        sum[0] = sum[1] = 0.f;
+    }
+    __device__ __forceinline__ void put(float* column) const {
+        column[first * 32] += sum[0];
+        if (first < E) column[(first + 1) * 32] += sum[1];
+    }
+    // a chunk within the two, its distances from lo to hi
+    __device__ __forceinline__ void add(const float (&v)[8], const int (&pk)[8], int pq, int lo, int hi) {
+        const float all = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+        if (hi < edge || first == E) {  // the last bucket has no upper neighbour
+            sum[0] += all;
+        } else if (lo >= edge) {
+            sum[1] += all;
+        } else {
+            float a[2] = {0.f, 0.f};
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const bool up = RelposBuckets::distance(pk[x], pq) >= edge;
+                a[0] += up ? 0.f : v[x];
+                a[1] += up ? v[x] : 0.f;
+            }
+            sum[0] += a[0];
+            sum[1] += a[1];
+        }
+    }
+};
+
+__device__ __forceinline__ void relpos_load8(const __nv_bfloat16* s, int n, uint4& w) {
+    if (n == 8) {
+        w = *reinterpret_cast<const uint4*>(s);
+    } else {
+        uint32_t v[8];
+#pragma unroll
+        for (int x = 0; x < 8; ++x) v[x] = x < n ? __bfloat16_as_ushort(s[x]) : 0u;
+        w = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+    }
+}
+__device__ __forceinline__ void relpos_values(const uint4& w, float (&v)[8]) {
+    v[0] = bf16lo(w.x); v[1] = bf16hi(w.x);
+    v[2] = bf16lo(w.y); v[3] = bf16hi(w.y);
+    v[4] = bf16lo(w.z); v[5] = bf16hi(w.z);
+    v[6] = bf16lo(w.w); v[7] = bf16hi(w.w);
+}
+
+__global__ void __launch_bounds__(kRelBwdWarps * 32, 5) tri_relpos_bwd_kernel(const __grid_constant__ RelposParams p) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const bool dead = device_error_pending();
     const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float* sums = reinterpret_cast<float*>(smem);  // [warps][nb][32]
     int32_t* sh_edges = reinterpret_cast<int32_t*>(sums + static_cast<size_t>(warps) * p.nb * 32);
     uint16_t* sh_lut = reinterpret_cast<uint16_t*>(sh_edges + 512);
-    for (int x = threadIdx.x; x < warps * p.nb * 32; x += blockDim.x) sums[x] = 0.f;
+    for (int x = threadIdx.x; x < warps * p.nb * 8; x += blockDim.x)
+        reinterpret_cast<float4*>(sums)[x] = make_float4(0.f, 0.f, 0.f, 0.f);
     RelposBuckets bucket;
     bucket.init(sh_edges, sh_lut, p);
 
     const int Hc = p.heads, S = 32 / Hc;
     const int h0 = blockIdx.y * Hc, h = h0 + lane / S, sub = lane % S;
-    const bool head = h < p.H;
     const int tiles = (p.chunks + S - 1) / S;
     float* mine = sums + static_cast<size_t>(warp) * p.nb * 32 + lane;
     const int64_t tasks = static_cast<int64_t>(p.B) * tiles * p.row_tasks;
@@ -206,7 +296,7 @@ __global__ void __launch_bounds__(kRelBwdWarps * 32) tri_relpos_bwd_kernel(const
         const int64_t bt = t / p.row_tasks;
         const int tile = static_cast<int>(bt % tiles), b = static_cast<int>(bt / tiles);
         const int c = tile * S + sub;
-        if (c >= p.chunks || !head) continue;  // no barrier or warp-wide step inside the walk
+        if (c >= p.chunks || h >= p.H) continue;  // no barrier or warp-wide step inside the walk
         const int j0 = c * 8, nj = min(8, p.Nk - j0);
         int pk[8], gk[8], pmin = INT32_MAX, pmax = INT32_MIN;
         bool one_group = true;
@@ -219,59 +309,95 @@ __global__ void __launch_bounds__(kRelBwdWarps * 32) tri_relpos_bwd_kernel(const
             pmax = max(pmax, pk[x]);
             one_group &= gk[x] == gk[0];
         }
-        const int i0 = rt * p.rows_per_task, i1 = min(p.Nq, i0 + p.rows_per_task);
         const __nv_bfloat16* src = p.dbias + b * p.ds[0] + h * p.ds[1] + j0;
-        int cur = 0;
-        float acc = 0.f;
-        for (int i = i0; i < i1; ++i) {
-            const int pq = p.pos_q[b * p.qs + i];
-            const int gq = p.grp_q ? p.grp_q[b * p.qs + i] : 0;
-            float v[8];
-            const __nv_bfloat16* s = src + i * p.ds[2];
-            if (nj == 8) {
-                const uint4 w = *reinterpret_cast<const uint4*>(s);
-                v[0] = bf16lo(w.x); v[1] = bf16hi(w.x);
-                v[2] = bf16lo(w.y); v[3] = bf16hi(w.y);
-                v[4] = bf16lo(w.z); v[5] = bf16hi(w.z);
-                v[6] = bf16lo(w.w); v[7] = bf16hi(w.w);
-            } else {
+        const int32_t* pos = p.pos_q + b * p.qs;
+        const int32_t* grp = p.grp_q ? p.grp_q + b * p.qs : nullptr;
+        RelposPair hand;
+        hand.take(bucket, 0);
+        float apart = 0.f;  // pairs of different groups
+        for (int i0 = rt * kRelRows; i0 < p.Nq; i0 += p.row_tasks * kRelRows) {
+            uint4 w[kRelRows];
+            int pq[kRelRows], gq[kRelRows];
 #pragma unroll
-                for (int x = 0; x < 8; ++x) v[x] = x < nj ? __bfloat162float(s[x]) : 0.f;
+            for (int u = 0; u < kRelRows; ++u) {
+                const int i = min(i0 + u, p.Nq - 1);
+                pq[u] = pos[i];
+                gq[u] = grp ? grp[i] : 0;
+                relpos_load8(src + i * p.ds[2], nj, w[u]);
             }
-            int k0 = p.E + 1, k1 = k0;
-            if (one_group && gk[0] == gq) {
-                k0 = bucket(pmin, pq);
-                k1 = bucket(pmax, pq);
-            } else if (!one_group) {
-                k1 = -1;
+            uint32_t more = 0;
+#pragma unroll
+            for (int u = 0; u < kRelRows; ++u) {
+                if (i0 + u >= p.Nq) break;
+                const int lo = RelposBuckets::distance(pmin, pq[u]), hi = RelposBuckets::distance(pmax, pq[u]);
+                float v[8];
+                relpos_values(w[u], v);
+                if (one_group && gk[0] != gq[u])
+                    apart += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
+                else if (one_group && lo >= hand.least && hi <= hand.most)
+                    hand.add(v, pk, pq[u], lo, hi);
+                else
+                    more |= 1u << u;
             }
-            if (k0 == k1) {
-                if (k0 != cur) {
-                    mine[cur * 32] += acc;
-                    acc = 0.f;
-                    cur = k0;
+            while (more) {
+                const int i = i0 + __ffs(more) - 1;
+                more &= more - 1;
+                uint4 wi;
+                float v[8];
+                relpos_load8(src + i * p.ds[2], nj, wi);
+                relpos_values(wi, v);
+                const int q = pos[i], g = grp ? grp[i] : 0;
+                const int lo = RelposBuckets::distance(pmin, q), hi = RelposBuckets::distance(pmax, q);
+                if (one_group) {  // and of the row's group
+                    if (lo < hand.least || hi > hand.most) {
+                        hand.put(mine);
+                        hand.take(bucket, bucket.of(lo));
+                    }
+                    if (hi <= hand.most) {
+                        hand.add(v, pk, q, lo, hi);
+                        continue;
+                    }
                 }
-                acc += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
-            } else {
+                // key by key; in ascending order of buckets (the usual case) equal neighbours are
+                // joined first, and what is left lies in different words
+                int k[8];
+                bool ascending = true;
 #pragma unroll
                 for (int x = 0; x < 8; ++x) {
-                    const int k = gk[x] == gq ? bucket(pk[x], pq) : p.E + 1;
-                    if (x < nj) mine[k * 32] += v[x];
+                    k[x] = gk[x] == g ? bucket.of(RelposBuckets::distance(pk[x], q)) : p.E + 1;
+                    if (x > 0) ascending &= k[x] >= k[x - 1];
+                }
+                if (ascending) {
+                    float old[8];
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) {
+                        if (x < 7 && k[x] == k[min(x + 1, 7)]) {
+                            v[min(x + 1, 7)] += v[x];
+                            k[x] = -1;
+                        }
+                        old[x] = k[x] >= 0 ? mine[k[x] * 32] : 0.f;
+                    }
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                        if (k[x] >= 0) mine[k[x] * 32] = old[x] + v[x];
+                } else {
+#pragma unroll
+                    for (int x = 0; x < 8; ++x)
+                        if (x < nj) mine[k[x] * 32] += v[x];
                 }
             }
         }
-        mine[cur * 32] += acc;
+        hand.put(mine);
+        if (p.grp_k) mine[(p.E + 1) * 32] += apart;
     }
     __syncthreads();
-    // the block's sums: over its warps, then over the chunks side by side
+    // the block's sums: a warp per bucket, over the warps, then over the chunks side by side
     float* out = p.partial + static_cast<int64_t>(blockIdx.x) * p.nb * p.H;
-    for (int x = threadIdx.x; x < p.nb * Hc; x += blockDim.x) {
-        const int k = x / Hc, hh = x - k * Hc;
-        if (h0 + hh >= p.H) continue;
+    for (int k = warp; k < p.nb; k += warps) {
         float s = 0.f;
-        for (int w = 0; w < warps; ++w)
-            for (int q = 0; q < S; ++q) s += sums[(static_cast<size_t>(w) * p.nb + k) * 32 + hh * S + q];
-        if (!dead) out[static_cast<int64_t>(k) * p.H + h0 + hh] = s;
+        for (int w = 0; w < warps; ++w) s += sums[(static_cast<size_t>(w) * p.nb + k) * 32 + lane];
+        for (int m = 1; m < S; m <<= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, m);
+        if (sub == 0 && h < p.H && !dead) out[static_cast<int64_t>(k) * p.H + h] = s;
     }
 }
 
