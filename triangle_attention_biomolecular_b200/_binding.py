@@ -13,6 +13,8 @@ import os
 import struct
 import threading
 
+import torch
+
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libtriattn.so")
 
@@ -534,201 +536,218 @@ def tri_gate_bwd(z, o, wg, wo, dy, dz, d_o, dwg, dwo, workspace, stream=None) ->
 #
 # The argument blocks are packed bytes (see _NORM_PACK, _RELPOS_PACK).  All
 # tensors of a call live on one CUDA device, which need not be the current one;
-# the call runs on the given stream, or that device's current stream.
+# the call runs on the given stream, or that device's current stream.  The small
+# calls are bound by what the host does, so tensors are described by plain
+# numbers here and no views are made of them.
 # ---------------------------------------------------------------------------
 
-def _run_on(where, tensors, stream, call):
-    """call(stream handle) with the device of `tensors` (None entries skipped) current; a
-    status other than 0 raises."""
-    import torch
-    dev = None
-    for t in tensors:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise TriAttnError(TRI_ATTN_ERR_UNSUPPORTED, f"{where}: every tensor must be on a CUDA device, got {t.device}")
-        if dev is None:
-            dev = t.device
-        elif t.device != dev:
-            raise TriAttnError(TRI_ATTN_ERR_UNSUPPORTED, f"{where}: tensors on {dev} and {t.device}")
+def _call(fn, args: bytes, where: str, stream, first, *others) -> None:
+    """fn(args, stream) on the device of the given tensors (None entries skipped); a status
+    other than 0 raises."""
+    dev = first.get_device()
+    if dev < 0:
+        raise TriAttnError(TRI_ATTN_ERR_UNSUPPORTED, f"{where}: every tensor must be on a CUDA device, got {first.device}")
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise TriAttnError(TRI_ATTN_ERR_UNSUPPORTED,
+                               f"{where}: every tensor must be on one CUDA device, got {first.device} and {t.device}")
     if stream is None:
-        stream = torch.cuda.current_stream(dev)
-    handle = stream if isinstance(stream, int) else stream.cuda_stream
-    if dev.index == torch.cuda.current_device():
-        st = call(handle)
+        stream = torch._C._cuda_getCurrentRawStream(dev)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if dev == torch._C._cuda_getDevice():
+        st = fn(args, stream)
     else:
         with torch.cuda.device(dev):
-            st = call(handle)
-    if st != TRI_ATTN_OK:
+            st = fn(args, stream)
+    if st:
         raise TriAttnError(st, where)
 
 
+_FLOAT_TYPES = {torch.bfloat16: TRI_TYPE_BF16, torch.float32: TRI_TYPE_F32}
+
+
 def _float_type(t, name) -> int:
-    import torch
-    if t.dtype is torch.bfloat16:
-        return TRI_TYPE_BF16
-    if t.dtype is torch.float32:
-        return TRI_TYPE_F32
-    raise TriAttnError(TRI_ATTN_ERR_DTYPE, f"{name} must be bfloat16 or float32, got {t.dtype}")
+    kind = _FLOAT_TYPES.get(t.dtype)
+    if kind is None:
+        raise TriAttnError(TRI_ATTN_ERR_DTYPE, f"{name} must be bfloat16 or float32, got {t.dtype}")
+    return kind
 
 
-def _rows(t, name, shape=None):
-    """(R, C) of a 2-D tensor of rows with unit channel stride."""
-    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
-        raise TriAttnError(TRI_ATTN_ERR_SHAPE, f"{name} must be {list(shape) if shape else '[R, C]'}, got {list(t.shape)}")
-    if t.shape[1] > 1 and t.stride(1) != 1:
-        raise TriAttnError(TRI_ATTN_ERR_STRIDE, f"{name}: the channels must have stride 1")
-    return tuple(t.shape)
+def _rows(t, name, want=None):
+    """(pointer, row stride, R, C) of rows of channels: a contiguous [..., C] tensor, or a 2-D one
+    with unit channel stride.  want: the (R, C) it must have."""
+    shape = t.shape
+    if not shape or not shape[-1]:
+        raise TriAttnError(TRI_ATTN_ERR_SHAPE, f"{name} must have rows of at least one channel, got {list(shape)}")
+    C = shape[-1]
+    R = t.numel() // C
+    if t.is_contiguous():
+        stride = C
+    elif len(shape) == 2 and (C == 1 or t.stride(1) == 1):
+        stride = t.stride(0)
+    else:
+        raise TriAttnError(TRI_ATTN_ERR_STRIDE, f"{name} must be contiguous, or 2-D with unit channel stride")
+    if want is not None and (R, C) != want:
+        raise TriAttnError(TRI_ATTN_ERR_SHAPE, f"{name} must have {want[0]} rows of {want[1]}, got {list(shape)}")
+    return t.data_ptr(), stride, R, C
 
 
-def _dense(t, name, dtype, shape):
-    if t.dtype != dtype:
+def _dense(t, name, dtype, shape) -> int:
+    """Pointer of a contiguous tensor that must have this dtype and shape; 0 for None."""
+    if t is None:
+        return 0
+    if t.dtype is not dtype:
         raise TriAttnError(TRI_ATTN_ERR_DTYPE, f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != shape or not t.is_contiguous():
+    if t.shape != shape or not t.is_contiguous():
         raise TriAttnError(TRI_ATTN_ERR_SHAPE, f"{name} must be a contiguous {list(shape)} tensor, got {list(t.shape)}")
+    return t.data_ptr()
 
 
 def _affine(w, b, C):
     """(w pointer, b pointer, type) of the norm's optional weight and bias."""
-    kind = TRI_TYPE_F32
-    for t, name in ((w, "weight"), (b, "bias")):
-        if t is not None:
-            kind = _float_type(t, name)
-            _dense(t, name, t.dtype, (C,))
-    if w is not None and b is not None and w.dtype != b.dtype:
+    if w is None and b is None:
+        return 0, 0, TRI_TYPE_F32
+    if w is not None and b is not None and w.dtype is not b.dtype:
         raise TriAttnError(TRI_ATTN_ERR_DTYPE, f"weight and bias must have one dtype, got {w.dtype} and {b.dtype}")
-    return 0 if w is None else w.data_ptr(), 0 if b is None else b.data_ptr(), kind
+    t = b if w is None else w
+    return _dense(w, "weight", t.dtype, (C,)), _dense(b, "bias", t.dtype, (C,)), _float_type(t, "weight and bias")
+
+
+_ACT8_TYPES = {TRI_ACT8_INT8: torch.int8, TRI_ACT8_E4M3: torch.float8_e4m3fn}
 
 
 def _act8(codes, exps, kind, R, C):
-    import torch
-    want = {TRI_ACT8_INT8: torch.int8, TRI_ACT8_E4M3: torch.float8_e4m3fn}.get(kind)
+    want = _ACT8_TYPES.get(kind)
     if want is None:
         raise TriAttnError(TRI_ATTN_ERR_UNSUPPORTED, f"kind must be TRI_ACT8_INT8 or TRI_ACT8_E4M3, got {kind}")
-    if codes.dtype != want or exps.dtype != torch.uint8:
+    if codes.dtype is not want or exps.dtype is not torch.uint8:
         raise TriAttnError(TRI_ATTN_ERR_DTYPE, f"codes must be {want} and exps uint8, got {codes.dtype} and {exps.dtype}")
-    _rows(codes, "codes", (R, C))
-    _rows(exps, "exps", (R, (C + 31) // 32))
-    return codes.data_ptr(), codes.stride(0), exps.data_ptr(), exps.stride(0), kind
+    cp, cs, _, _ = _rows(codes, "codes", (R, C))
+    ep, es, _, _ = _rows(exps, "exps", (R, (C + 31) // 32))
+    return cp, cs, ep, es, kind
 
 
 _NO_ACT8 = (0, 0, 0, 0, TRI_ACT8_NONE)
 
 
+def _workspace(t):
+    if t is None:
+        return 0, 0
+    if t.dtype is not torch.uint8 or not t.is_contiguous():
+        raise TriAttnError(TRI_ATTN_ERR_DTYPE, "workspace must be a contiguous uint8 tensor")
+    return t.data_ptr(), t.numel()
+
+
 def tri_norm_fwd(x, w, b, y, stats, codes=None, exps=None, kind: int = 0, eps: float = 1e-5, stream=None) -> None:
-    """y = (x - mean) * rstd * w + b over the channels of each row; x, y BF16 or FP32 [R, C]
-    (rows may be padded), w, b [C] or None, stats FP32 [2, R] written (means, rstds).  With
-    kind set, codes [R, C] and exps [R, ceil(C/32)] get x in 8 bits in the same pass."""
-    import torch
-    R, C = _rows(x, "x")
-    _rows(y, "y", (R, C))
-    _dense(stats, "stats", torch.float32, (2, R))
+    """y = (x - mean) * rstd * w + b over the channels of each row; x, y BF16 or FP32, contiguous
+    [..., C] or [R, C] with padded rows, w, b [C] or None, stats FP32 [2, R] written (means,
+    rstds).  With kind set, codes [.., C] and exps [.., ceil(C/32)] get x in 8 bits in the same
+    pass."""
+    xp, xs, R, C = _rows(x, "x")
+    yp, ys, _, _ = _rows(y, "y", (R, C))
+    sp = _dense(stats, "stats", torch.float32, (2, R))
     wp, bp, wt = _affine(w, b, C)
     act = _act8(codes, exps, kind, R, C) if kind else _NO_ACT8
-    a = _NORM_PACK.pack(R, x.data_ptr(), x.stride(0), wp, bp, y.data_ptr(), y.stride(0), stats.data_ptr(), *act, C,
-                        _float_type(x, "x"), wt, _float_type(y, "y"), eps)
-    lib = load()
-    _run_on("tri_norm_fwd", (x, w, b, y, stats, codes, exps), stream, lambda s: lib.tri_norm_fwd(a, s))
+    a = _NORM_PACK.pack(R, xp, xs, wp, bp, yp, ys, sp, *act, C, _float_type(x, "x"), wt, _float_type(y, "y"), eps)
+    _call((_lib or load()).tri_norm_fwd, a, "tri_norm_fwd", stream, x, w, b, y, stats, codes, exps)
 
 
 def tri_norm_restore(codes, exps, kind: int, stats, w, b, y, stream=None) -> None:
     """The norm's output once more from what tri_norm_fwd kept: x in 8 bits and its stats."""
-    import torch
-    R, C = _rows(y, "y")
-    _dense(stats, "stats", torch.float32, (2, R))
+    yp, ys, R, C = _rows(y, "y")
+    sp = _dense(stats, "stats", torch.float32, (2, R))
     wp, bp, wt = _affine(w, b, C)
-    a = _NORM_PACK.pack(R, 0, 0, wp, bp, y.data_ptr(), y.stride(0), stats.data_ptr(),
-                        *_act8(codes, exps, kind, R, C), C, 0, wt, _float_type(y, "y"), 0.0)
-    lib = load()
-    _run_on("tri_norm_restore", (codes, exps, stats, w, b, y), stream, lambda s: lib.tri_norm_restore(a, s))
+    a = _NORM_PACK.pack(R, 0, 0, wp, bp, yp, ys, sp, *_act8(codes, exps, kind, R, C), C, 0, wt, _float_type(y, "y"), 0.0)
+    _call((_lib or load()).tri_norm_restore, a, "tri_norm_restore", stream, codes, exps, stats, w, b, y)
 
 
 def tri_norm_bwd_workspace_bytes(R: int, C: int) -> int:
-    return int(load().tri_norm_bwd_workspace_bytes(R, C))
+    return (_lib or load()).tri_norm_bwd_workspace_bytes(R, C)
 
 
 def tri_norm_bwd(x, codes, exps, kind: int, stats, w, dy, dx, dw, db, workspace, stream=None) -> None:
-    """Gradients of the norm for the upstream dy [R, C].  x is the forward's input, or None
-    with kind, codes and exps set: its 8-bit form.  dx [R, C] has x's dtype (or None); dw, db
-    FP32 [C] (or both None); workspace a uint8 CUDA tensor of at least
-    tri_norm_bwd_workspace_bytes(R, C) bytes (None without dw and db)."""
-    import torch
-    R, C = _rows(dy, "dy")
-    _dense(stats, "stats", torch.float32, (2, R))
+    """Gradients of the norm for the upstream dy.  x is the forward's input, or None with kind,
+    codes and exps set: its 8-bit form.  dx has x's dtype (or is None); dw, db FP32 [C] (or both
+    None); workspace a uint8 CUDA tensor of at least tri_norm_bwd_workspace_bytes(R, C) bytes
+    (None without dw and db)."""
+    dyp, dys, R, C = _rows(dy, "dy")
+    sp = _dense(stats, "stats", torch.float32, (2, R))
     if (x is None) == (not kind):
         raise TriAttnError(TRI_ATTN_ERR_NULL, "tri_norm_bwd: either x or its 8-bit form must be given")
     if x is not None:
-        _rows(x, "x", (R, C))
-        xs, act, xt = (x.data_ptr(), x.stride(0)), _NO_ACT8, _float_type(x, "x")
+        xp, xs, _, _ = _rows(x, "x", (R, C))
+        act, xt = _NO_ACT8, _float_type(x, "x")
     else:
-        xs, act, xt = (0, 0), _act8(codes, exps, kind, R, C), TRI_TYPE_BF16
-    dxs = (0, 0)
+        xp, xs, act, xt = 0, 0, _act8(codes, exps, kind, R, C), TRI_TYPE_BF16
+    dxp, dxs = 0, 0
     if dx is not None:
-        _rows(dx, "dx", (R, C))
-        if x is not None and dx.dtype != x.dtype:
+        dxp, dxs, _, _ = _rows(dx, "dx", (R, C))
+        if x is not None and dx.dtype is not x.dtype:
             raise TriAttnError(TRI_ATTN_ERR_DTYPE, f"dx must be {x.dtype}, got {dx.dtype}")
-        dxs, xt = (dx.data_ptr(), dx.stride(0)), _float_type(dx, "dx")
+        xt = _float_type(dx, "dx")
     if (dw is None) != (db is None):
         raise TriAttnError(TRI_ATTN_ERR_NULL, "tri_norm_bwd: dw and db are given together or not at all")
-    for t, n in ((dw, "dw"), (db, "db")):
-        if t is not None:
-            _dense(t, n, torch.float32, (C,))
     wp, _, wt = _affine(w, None, C)
-    ws = (0, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
-    a = _NORM_PACK.pack(R, *xs, wp, 0, 0, 0, stats.data_ptr(), *act, C, xt, wt, _float_type(dy, "dy"), 0.0)
-    a += _NORM_TAIL.pack(dy.data_ptr(), dy.stride(0), *dxs, 0 if dw is None else dw.data_ptr(),
-                         0 if db is None else db.data_ptr(), *ws)
-    lib = load()
-    _run_on("tri_norm_bwd", (dy, x, codes, exps, stats, w, dx, dw, db, workspace), stream,
-            lambda s: lib.tri_norm_bwd(a, s))
+    a = _NORM_PACK.pack(R, xp, xs, wp, 0, 0, 0, sp, *act, C, xt, wt, _float_type(dy, "dy"), 0.0) + \
+        _NORM_TAIL.pack(dyp, dys, dxp, dxs, _dense(dw, "dw", torch.float32, (C,)), _dense(db, "db", torch.float32, (C,)),
+                        *_workspace(workspace))
+    _call((_lib or load()).tri_norm_bwd, a, "tri_norm_bwd", stream, dy, x, codes, exps, stats, w, dx, dw, db, workspace)
 
 
 def tri_act8_pack(x, codes, exps, kind: int, stream=None) -> None:
-    """codes [R, C], exps [R, ceil(C/32)] = x [R, C] (BF16 or FP32) in 8 bits."""
-    R, C = _rows(x, "x")
-    act, xt = Act8(*_act8(codes, exps, kind, R, C)), _float_type(x, "x")
-    lib = load()
-    _run_on("tri_act8_pack", (x, codes, exps), stream,
-            lambda s: lib.tri_act8_pack(R, C, x.data_ptr(), x.stride(0), xt, act, s))
+    """codes [.., C], exps [.., ceil(C/32)] = x [.., C] (BF16 or FP32) in 8 bits."""
+    xp, xs, R, C = _rows(x, "x")
+    act, xt, lib = Act8(*_act8(codes, exps, kind, R, C)), _float_type(x, "x"), _lib or load()
+    _call(lambda a, s: lib.tri_act8_pack(R, C, xp, xs, xt, a, s), act, "tri_act8_pack", stream, x, codes, exps)
 
 
 def tri_act8_unpack(codes, exps, kind: int, x, stream=None) -> None:
-    """x [R, C] (BF16 or FP32) = the values that codes and exps stand for."""
-    R, C = _rows(x, "x")
-    act, xt = Act8(*_act8(codes, exps, kind, R, C)), _float_type(x, "x")
-    lib = load()
-    _run_on("tri_act8_unpack", (x, codes, exps), stream,
-            lambda s: lib.tri_act8_unpack(R, C, act, x.data_ptr(), x.stride(0), xt, s))
+    """x [.., C] (BF16 or FP32) = the values that codes and exps stand for."""
+    xp, xs, R, C = _rows(x, "x")
+    act, xt, lib = Act8(*_act8(codes, exps, kind, R, C)), _float_type(x, "x"), _lib or load()
+    _call(lambda a, s: lib.tri_act8_unpack(R, C, a, xp, xs, xt, s), act, "tri_act8_unpack", stream, x, codes, exps)
+
+
+def _int32(t, name, dims) -> int:
+    if t is None:
+        return 0
+    if t.dtype is not torch.int32:
+        raise TriAttnError(TRI_ATTN_ERR_DTYPE, f"{name} must be torch.int32, got {t.dtype}")
+    if t.dim() != dims:
+        raise TriAttnError(TRI_ATTN_ERR_SHAPE, f"{name} must have {dims} dims")
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise TriAttnError(TRI_ATTN_ERR_STRIDE, f"{name} must have unit inner stride")
+    return t.data_ptr()
 
 
 def _relpos_index(pos_q, pos_k, group_q, group_k, edges):
-    import torch
+    """(E, edges pointer, the positions' and groups' pointers, batch strides)."""
     if (group_q is None) != (group_k is None):
         raise TriAttnError(TRI_ATTN_ERR_NULL, "group_q and group_k are given together or not at all")
-    for t, n, d in ((pos_q, "pos_q", 2), (pos_k, "pos_k", 2), (group_q, "group_q", 2), (group_k, "group_k", 2),
-                    (edges, "edges", 1)):
-        if t is None:
-            continue
-        _check_tensor(t, n, torch.int32, d)
-        if t.shape[-1] > 1 and t.stride(-1) != 1:
-            raise TriAttnError(TRI_ATTN_ERR_STRIDE, f"{n} must have unit inner stride")
-    for g, t, n in ((group_q, pos_q, "group_q"), (group_k, pos_k, "group_k")):
-        if g is not None and (g.shape != t.shape or (t.shape[0] > 1 and g.stride(0) != t.stride(0))):
-            raise TriAttnError(TRI_ATTN_ERR_SHAPE, f"{n} must be laid out as its positions are")
-    if pos_q.shape[0] != pos_k.shape[0]:
+    idx = (_int32(edges, "edges", 1), _int32(pos_q, "pos_q", 2), _int32(pos_k, "pos_k", 2),
+           _int32(group_q, "group_q", 2), _int32(group_k, "group_k", 2), pos_q.stride(0), pos_k.stride(0))
+    B = pos_q.shape[0]
+    if B != pos_k.shape[0]:
         raise TriAttnError(TRI_ATTN_ERR_SHAPE, "pos_q and pos_k must have one batch size")
-    ptr = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
-    return (ptr(edges), ptr(pos_q), ptr(pos_k), ptr(group_q), ptr(group_k), pos_q.stride(0), pos_k.stride(0))
+    if group_q is not None:
+        for g, p, n in ((group_q, pos_q, "group_q"), (group_k, pos_k, "group_k")):
+            if g.shape != p.shape or (B > 1 and g.stride(0) != p.stride(0)):
+                raise TriAttnError(TRI_ATTN_ERR_SHAPE, f"{n} must be laid out as its positions are")
+    return idx
 
 
-def _relpos_bias(t, name, B, H, Nq, Nk):
+def _relpos_bias(t, name, shape):
     if t is None:
         return 0, 0, 0, 0, 0
-    v = _v4(t, name)
-    if tuple(t.shape) != (B, H, Nq, Nk):
-        raise TriAttnError(TRI_ATTN_ERR_SHAPE, f"{name} must be {[B, H, Nq, Nk]}, got {list(t.shape)}")
-    # the stride of a dimension of one element means nothing: any multiple of 8 will do
-    return v[0], *(s if n > 1 else 0 for s, n in zip(v[1:4], t.shape)), v[4] if Nk > 1 else 1
+    if t.dtype is not torch.bfloat16:
+        raise TriAttnError(TRI_ATTN_ERR_DTYPE, f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.shape != shape:
+        raise TriAttnError(TRI_ATTN_ERR_SHAPE, f"{name} must be {list(shape)}, got {list(t.shape)}")
+    # the stride of a dimension of one element means nothing: 0 (1 for the keys) will do
+    B, H, Nq, Nk = shape
+    s0, s1, s2, s3 = t.stride()
+    return t.data_ptr(), s0 if B > 1 else 0, s1 if H > 1 else 0, s2 if Nq > 1 else 0, s3 if Nk > 1 else 1
 
 
 def tri_relpos_fwd(table, edges, pos_q, pos_k, group_q, group_k, base, bias, stream=None) -> None:
@@ -740,32 +759,30 @@ def tri_relpos_fwd(table, edges, pos_q, pos_k, group_q, group_k, base, bias, str
     (nb, H), (B, Nq), Nk, E = table.shape, pos_q.shape, pos_k.shape[1], edges.shape[0]
     if nb != E + 1 + (group_q is not None):
         raise TriAttnError(TRI_ATTN_ERR_SHAPE, f"table must have {E + 1 + (group_q is not None)} rows, got {nb}")
+    shape = (B, H, Nq, Nk)
     a = _RELPOS_PACK.pack(B, H, Nq, Nk, E, _float_type(table, "table"), table.data_ptr(), *idx,
-                          *_relpos_bias(base, "base", B, H, Nq, Nk), *_relpos_bias(bias, "bias", B, H, Nq, Nk))
-    lib = load()
-    _run_on("tri_relpos_fwd", (table, edges, pos_q, pos_k, group_q, group_k, base, bias), stream,
-            lambda s: lib.tri_relpos_fwd(a, s))
+                          *_relpos_bias(base, "base", shape), *_relpos_bias(bias, "bias", shape))
+    _call((_lib or load()).tri_relpos_fwd, a, "tri_relpos_fwd", stream, table, edges, pos_q, pos_k, group_q, group_k,
+          base, bias)
 
 
 def tri_relpos_bwd_workspace_bytes(B: int, H: int, Nq: int, Nk: int, E: int, groups: bool) -> int:
-    return int(load().tri_relpos_bwd_workspace_bytes(B, H, Nq, Nk, E, int(groups)))
+    return (_lib or load()).tri_relpos_bwd_workspace_bytes(B, H, Nq, Nk, E, groups)
 
 
 def tri_relpos_bwd(dbias, edges, pos_q, pos_k, group_q, group_k, dtable, workspace, stream=None) -> None:
     """dtable [buckets, H] (FP32) = the sums of dbias (BF16 [B,H,Nq,Nk]) by bucket; workspace a
     uint8 CUDA tensor of at least tri_relpos_bwd_workspace_bytes(...) bytes."""
-    import torch
     idx = _relpos_index(pos_q, pos_k, group_q, group_k, edges)
     if dbias.dim() != 4:
         raise TriAttnError(TRI_ATTN_ERR_SHAPE, "dbias must be [B, H, Nq, Nk]")
     (B, Nq), Nk, E, H = pos_q.shape, pos_k.shape[1], edges.shape[0], dbias.shape[1]
-    _dense(dtable, "dtable", torch.float32, (E + 1 + (group_q is not None), H))
-    a = _RELPOS_PACK.pack(B, H, Nq, Nk, E, 0, 0, *idx, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0)
-    a += _RELPOS_TAIL.pack(*_relpos_bias(dbias, "dbias", B, H, Nq, Nk), dtable.data_ptr(), workspace.data_ptr(),
-                           workspace.numel() * workspace.element_size())
-    lib = load()
-    _run_on("tri_relpos_bwd", (dbias, edges, pos_q, pos_k, group_q, group_k, dtable, workspace), stream,
-            lambda s: lib.tri_relpos_bwd(a, s))
+    a = _RELPOS_PACK.pack(B, H, Nq, Nk, E, 0, 0, *idx, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0) + \
+        _RELPOS_TAIL.pack(*_relpos_bias(dbias, "dbias", (B, H, Nq, Nk)),
+                          _dense(dtable, "dtable", torch.float32, (E + 1 + (group_q is not None), H)),
+                          *_workspace(workspace))
+    _call((_lib or load()).tri_relpos_bwd, a, "tri_relpos_bwd", stream, dbias, edges, pos_q, pos_k, group_q, group_k,
+          dtable, workspace)
 
 
 def tri_attn_device_error(clear: bool = True):

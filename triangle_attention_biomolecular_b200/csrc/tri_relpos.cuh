@@ -47,8 +47,8 @@ struct RelposBuckets {
     const uint16_t* lut;
     int E, lo, size, dmin, dmax;
 
-    // number of edges <= d
-    __device__ __forceinline__ int search(int d) const {
+    // number of edges <= d; rarely needed, so one copy of the code
+    __device__ __noinline__ int search(int d) const {
         int n = 0;
 #pragma unroll 1
         for (int s = 256; s > 0; s >>= 1)
@@ -86,6 +86,23 @@ struct RelposBuckets {
         d = min(max(d, dmin), dmax);
         const uint32_t x = static_cast<uint32_t>(d) - static_cast<uint32_t>(lo);
         return x < static_cast<uint32_t>(size) ? lut[x] : search(d);
+    }
+    // eight at once, their look-ups in flight together
+    __device__ __forceinline__ void of8(const int (&d)[8], int (&k)[8]) const {
+        bool far[8], any = false;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+            const int dx = min(max(d[x], dmin), dmax);
+            const uint32_t at = static_cast<uint32_t>(dx) - static_cast<uint32_t>(lo);
+            far[x] = at >= static_cast<uint32_t>(size);
+            any |= far[x];
+            k[x] = lut[far[x] ? 0u : at];
+        }
+        if (any) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+                if (far[x]) k[x] = search(d[x]);
+        }
     }
     // the distances of bucket k are least(k) <= d <= most(k)
     __device__ __forceinline__ int least(int k) const { return k > 0 ? edges[k - 1] : INT32_MIN; }
@@ -154,9 +171,12 @@ __global__ void __launch_bounds__(kRelThreads) tri_relpos_fwd_kernel(const __gri
 #pragma unroll
             for (int x = 0; x < 8; ++x) at[x] = first * pitch;
         } else {
+            int k[8];
 #pragma unroll
-            for (int x = 0; x < 8; ++x)
-                at[x] = (at[x] ? p.E + 1 : bucket.of(RelposBuckets::distance(key[x], pq))) * pitch;
+            for (int x = 0; x < 8; ++x) key[x] = RelposBuckets::distance(key[x], pq);
+            bucket.of8(key, k);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) at[x] = (at[x] ? p.E + 1 : k[x]) * pitch;
         }
         __nv_bfloat16* out = p.bias + b * p.os[0] + h0 * p.os[1] + i * p.os[2] + j0;
         const __nv_bfloat16* in = BASE ? p.base + b * p.bs[0] + h0 * p.bs[1] + i * p.bs[2] + j0 : nullptr;
@@ -218,41 +238,36 @@ __host__ constexpr size_t relpos_bwd_smem(int nb, int warps) {
     return static_cast<size_t>(warps) * nb * 32 * 4 + 512 * 4 + kRelLut * 2;
 }
 
-// the two buckets a lane has in hand: first and first + 1
+// the two buckets a lane has in hand: first and, if there is one, first + 1
 struct RelposPair {
-    int first, E;
-    int least, edge, most;  // distances least .. edge - 1 and edge .. most
-    float sum[2];
+    int first, least, edge, most;  // distances least .. edge - 1 and edge .. most
+    float sum0, sum1;
     __device__ __forceinline__ void take(const RelposBuckets& bucket, int k) {
         first = k;
-        E = bucket.E;
         least = bucket.least(k);
         edge = k < bucket.E ? bucket.edges[k] : INT32_MAX;
         most = bucket.most(min(k + 1, bucket.E));
-        sum[0] = sum[1] = 0.f;
+        sum0 = sum1 = 0.f;
     }
-    __device__ __forceinline__ void put(float* column) const {
-        column[first * 32] += sum[0];
-        if (first < E) column[(first + 1) * 32] += sum[1];
-    }
-    // a chunk within the two, its distances from lo to hi
-    __device__ __forceinline__ void add(const float (&v)[8], const int (&pk)[8], int pq, int lo, int hi) {
-        const float all = ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
-        if (hi < edge || first == E) {  // the last bucket has no upper neighbour
-            sum[0] += all;
-        } else if (lo >= edge) {
-            sum[1] += all;
+    __device__ __forceinline__ void put(float* column, int E) const {
+        if (first < E) {
+            column[first * 32] += sum0;
+            column[(first + 1) * 32] += sum1;
         } else {
-            float a[2] = {0.f, 0.f};
-#pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                const bool up = RelposBuckets::distance(pk[x], pq) >= edge;
-                a[0] += up ? 0.f : v[x];
-                a[1] += up ? v[x] : 0.f;
-            }
-            sum[0] += a[0];
-            sum[1] += a[1];
+            column[E * 32] += sum0 + sum1;
         }
+    }
+    // a chunk across the edge
+    __device__ __forceinline__ void split(const float (&v)[8], const int (&pk)[8], int pq) {
+        float a = 0.f, b = 0.f;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+            const bool up = RelposBuckets::distance(pk[x], pq) >= edge;
+            a += up ? 0.f : v[x];
+            b += up ? v[x] : 0.f;
+        }
+        sum0 += a;
+        sum1 += b;
     }
 };
 
@@ -271,6 +286,13 @@ __device__ __forceinline__ void relpos_values(const uint4& w, float (&v)[8]) {
     v[2] = bf16lo(w.y); v[3] = bf16hi(w.y);
     v[4] = bf16lo(w.z); v[5] = bf16hi(w.z);
     v[6] = bf16lo(w.w); v[7] = bf16hi(w.w);
+}
+
+__device__ __forceinline__ float relpos_sum8(const float (&v)[8]) {
+    const float2 a = fadd2(make_float2(v[0], v[1]), make_float2(v[2], v[3]));
+    const float2 b = fadd2(make_float2(v[4], v[5]), make_float2(v[6], v[7]));
+    const float2 c = fadd2(a, b);
+    return c.x + c.y;
 }
 
 __global__ void __launch_bounds__(kRelBwdWarps * 32, 5) tri_relpos_bwd_kernel(const __grid_constant__ RelposParams p) {
@@ -318,26 +340,42 @@ __global__ void __launch_bounds__(kRelBwdWarps * 32, 5) tri_relpos_bwd_kernel(co
         for (int i0 = rt * kRelRows; i0 < p.Nq; i0 += p.row_tasks * kRelRows) {
             uint4 w[kRelRows];
             int pq[kRelRows], gq[kRelRows];
+            const __nv_bfloat16* s = src + i0 * p.ds[2];
+            const int rows = min(kRelRows, p.Nq - i0);
+            if (rows == kRelRows) {
 #pragma unroll
-            for (int u = 0; u < kRelRows; ++u) {
-                const int i = min(i0 + u, p.Nq - 1);
-                pq[u] = pos[i];
-                gq[u] = grp ? grp[i] : 0;
-                relpos_load8(src + i * p.ds[2], nj, w[u]);
+                for (int u = 0; u < kRelRows; ++u, s += p.ds[2]) {
+                    pq[u] = pos[i0 + u];
+                    gq[u] = grp ? grp[i0 + u] : 0;
+                    relpos_load8(s, nj, w[u]);
+                }
+            } else {
+#pragma unroll
+                for (int u = 0; u < kRelRows; ++u, s += p.ds[2]) {
+                    pq[u] = gq[u] = 0;
+                    if (u < rows) {
+                        pq[u] = pos[i0 + u];
+                        gq[u] = grp ? grp[i0 + u] : 0;
+                        relpos_load8(s, nj, w[u]);
+                    }
+                }
             }
             uint32_t more = 0;
 #pragma unroll
             for (int u = 0; u < kRelRows; ++u) {
-                if (i0 + u >= p.Nq) break;
+                if (u >= rows) break;
                 const int lo = RelposBuckets::distance(pmin, pq[u]), hi = RelposBuckets::distance(pmax, pq[u]);
                 float v[8];
                 relpos_values(w[u], v);
-                if (one_group && gk[0] != gq[u])
-                    apart += ((v[0] + v[1]) + (v[2] + v[3])) + ((v[4] + v[5]) + (v[6] + v[7]));
-                else if (one_group && lo >= hand.least && hi <= hand.most)
-                    hand.add(v, pk, pq[u], lo, hi);
-                else
-                    more |= 1u << u;
+                const float all = relpos_sum8(v);
+                const bool other = one_group && gk[0] != gq[u];
+                const bool fits = one_group && !other && lo >= hand.least && hi <= hand.most;
+                const bool below = fits && hi < hand.edge, above = fits && lo >= hand.edge;
+                apart += other ? all : 0.f;
+                hand.sum0 += below ? all : 0.f;
+                hand.sum1 += above ? all : 0.f;
+                if (fits && !below && !above) hand.split(v, pk, pq[u]);
+                if (!other && !fits) more |= 1u << u;
             }
             while (more) {
                 const int i = i0 + __ffs(more) - 1;
@@ -347,24 +385,27 @@ __global__ void __launch_bounds__(kRelBwdWarps * 32, 5) tri_relpos_bwd_kernel(co
                 relpos_load8(src + i * p.ds[2], nj, wi);
                 relpos_values(wi, v);
                 const int q = pos[i], g = grp ? grp[i] : 0;
-                const int lo = RelposBuckets::distance(pmin, q), hi = RelposBuckets::distance(pmax, q);
                 if (one_group) {  // and of the row's group
+                    const int lo = RelposBuckets::distance(pmin, q), hi = RelposBuckets::distance(pmax, q);
                     if (lo < hand.least || hi > hand.most) {
-                        hand.put(mine);
+                        hand.put(mine, p.E);
                         hand.take(bucket, bucket.of(lo));
                     }
                     if (hi <= hand.most) {
-                        hand.add(v, pk, q, lo, hi);
+                        hand.split(v, pk, q);
                         continue;
                     }
                 }
                 // key by key; in ascending order of buckets (the usual case) equal neighbours are
                 // joined first, and what is left lies in different words
-                int k[8];
+                int d[8], k[8];
+#pragma unroll
+                for (int x = 0; x < 8; ++x) d[x] = RelposBuckets::distance(pk[x], q);
+                bucket.of8(d, k);
                 bool ascending = true;
 #pragma unroll
                 for (int x = 0; x < 8; ++x) {
-                    k[x] = gk[x] == g ? bucket.of(RelposBuckets::distance(pk[x], q)) : p.E + 1;
+                    if (gk[x] != g) k[x] = p.E + 1;
                     if (x > 0) ascending &= k[x] >= k[x - 1];
                 }
                 if (ascending) {
@@ -387,12 +428,13 @@ __global__ void __launch_bounds__(kRelBwdWarps * 32, 5) tri_relpos_bwd_kernel(co
                 }
             }
         }
-        hand.put(mine);
+        hand.put(mine, p.E);
         if (p.grp_k) mine[(p.E + 1) * 32] += apart;
     }
     __syncthreads();
     // the block's sums: a warp per bucket, over the warps, then over the chunks side by side
     float* out = p.partial + static_cast<int64_t>(blockIdx.x) * p.nb * p.H;
+#pragma unroll 4
     for (int k = warp; k < p.nb; k += warps) {
         float s = 0.f;
         for (int w = 0; w < warps; ++w) s += sums[(static_cast<size_t>(w) * p.nb + k) * 32 + lane];

@@ -55,44 +55,46 @@ def _kind(name: str):
 
 
 def _rows(x: torch.Tensor) -> torch.Tensor:
-    """x as [R, C] rows with unit channel stride, without a copy where its strides allow it."""
-    if x.dim() < 1 or x.shape[-1] < 1:
-        raise B.TriAttnError(B.TRI_ATTN_ERR_SHAPE, f"a tensor of rows of at least one channel is needed, got {list(x.shape)}")
-    C = x.shape[-1]
-    R = x.numel() // C
-    if x.is_contiguous():
-        return x.view(R, C)
-    if x.stride(-1) == 1:
+    """x itself if its rows can be walked as they lie (contiguous, or 2-D with unit channel
+    stride), else as an [R, C] view or, where no view does, a contiguous copy."""
+    if x.is_contiguous() or (x.dim() == 2 and x.stride(1) == 1):
+        return x
+    if x.dim() > 2 and x.stride(-1) == 1:
         try:
-            return x.view(R, C)
+            return x.view(-1, x.shape[-1])
         except RuntimeError:
             pass
-    return x.contiguous().view(R, C)
+    return x.contiguous()
 
 
 def _param(p: Optional[torch.Tensor]):
     return None if p is None else p.contiguous()
 
 
+def _empty(x: torch.Tensor, dtype: Optional[torch.dtype]) -> torch.Tensor:
+    """An uninitialised contiguous tensor of x's shape."""
+    if x.is_contiguous() and (dtype is None or dtype is x.dtype):
+        return torch.empty_like(x)
+    return x.new_empty(x.shape, dtype=dtype)
+
+
 def _empty8(x: torch.Tensor, kind: str):
     _, dt = _kind(kind)
-    codes = torch.empty(x.shape, dtype=dt, device=x.device)
-    exps = torch.empty((*x.shape[:-1], (x.shape[-1] + 31) // 32), dtype=torch.uint8, device=x.device)
-    return Act8(codes, exps, x.dtype)
+    *lead, C = x.shape
+    return Act8(x.new_empty(x.shape, dtype=dt), x.new_empty((*lead, (C + 31) // 32), dtype=torch.uint8), x.dtype)
 
 
 def act8_pack(x: torch.Tensor, kind: str = "int8") -> Act8:
     """x (BF16 or FP32, [..., C]) in 8 bits."""
-    x2 = _rows(x)
     a = _empty8(x, kind)
-    B.tri_act8_pack(x2, _rows(a.codes), _rows(a.exps), a.kind)
+    B.tri_act8_pack(_rows(x), a.codes, a.exps, a.kind)
     return a
 
 
 def act8_unpack(a: Act8, dtype: Optional[torch.dtype] = None) -> torch.Tensor:
     """The values a stands for, in ``dtype`` (default: the dtype that was packed)."""
-    x = torch.empty(a.codes.shape, dtype=dtype or a.dtype, device=a.codes.device)
-    B.tri_act8_unpack(_rows(a.codes), _rows(a.exps), a.kind, _rows(x))
+    x = a.codes.new_empty(a.codes.shape, dtype=dtype or a.dtype)
+    B.tri_act8_unpack(_rows(a.codes), _rows(a.exps), a.kind, x)
     return x
 
 
@@ -101,22 +103,22 @@ def norm_forward(x, weight=None, bias=None, eps: float = 1e-5, out_dtype: Option
     """Returns (y, stats, kept): y of x's shape in ``out_dtype`` (default: x's dtype), stats FP32
     [2, rows] (means, reciprocal standard deviations), and kept, x as an :class:`Act8` written
     in the same pass (None without ``checkpoint``)."""
-    x2 = _rows(x)
-    y = torch.empty(x.shape, dtype=out_dtype or x.dtype, device=x.device)
-    stats = torch.empty((2, x2.shape[0]), dtype=torch.float32, device=x.device)
-    weight, bias = _param(weight), _param(bias)
+    if not x.dim() or not x.shape[-1]:
+        raise B.TriAttnError(B.TRI_ATTN_ERR_SHAPE, f"x must have rows of at least one channel, got {list(x.shape)}")
+    y = _empty(x, out_dtype)
+    stats = x.new_empty((2, x.numel() // x.shape[-1]), dtype=torch.float32)
     if checkpoint is None:
-        B.tri_norm_fwd(x2, weight, bias, _rows(y), stats, eps=eps)
+        B.tri_norm_fwd(_rows(x), _param(weight), _param(bias), y, stats, eps=eps)
         return y, stats, None
     a = _empty8(x, checkpoint)
-    B.tri_norm_fwd(x2, weight, bias, _rows(y), stats, _rows(a.codes), _rows(a.exps), a.kind, eps)
+    B.tri_norm_fwd(_rows(x), _param(weight), _param(bias), y, stats, a.codes, a.exps, a.kind, eps)
     return y, stats, a
 
 
 def norm_restore(kept: Act8, stats, weight=None, bias=None, out_dtype: Optional[torch.dtype] = None):
     """The norm's output from the 8-bit x and the statistics of :func:`norm_forward`."""
-    y = torch.empty(kept.codes.shape, dtype=out_dtype or kept.dtype, device=kept.codes.device)
-    B.tri_norm_restore(_rows(kept.codes), _rows(kept.exps), kept.kind, stats, _param(weight), _param(bias), _rows(y))
+    y = kept.codes.new_empty(kept.codes.shape, dtype=out_dtype or kept.dtype)
+    B.tri_norm_restore(_rows(kept.codes), _rows(kept.exps), kept.kind, stats, _param(weight), _param(bias), y)
     return y
 
 
@@ -124,18 +126,17 @@ def norm_backward(x, stats, dy, weight=None, need_dx: bool = True, need_dw: Opti
     """Returns (dx, dweight, dbias) for the upstream gradient dy; ``x`` is the forward's input or
     the :class:`Act8` it kept.  dx has x's dtype; dweight and dbias are FP32 [C] (None unless
     ``need_dw``, by default when there is a weight)."""
-    dy2 = _rows(dy)
-    R, C = dy2.shape
-    kept = isinstance(x, Act8)
-    x2, codes, exps, kind = (None, _rows(x.codes), _rows(x.exps), x.kind) if kept else (_rows(x), None, None, 0)
     dx = dw = db = ws = None
     if need_dx:
-        dx = torch.empty(dy.shape, dtype=x.dtype, device=dy.device)
+        dx = _empty(dy, x.dtype)
     if weight is not None if need_dw is None else need_dw:
-        grads = torch.empty((2, C), dtype=torch.float32, device=dy.device)
-        dw, db = grads[0], grads[1]
-        ws = torch.empty(B.tri_norm_bwd_workspace_bytes(R, C), dtype=torch.uint8, device=dy.device)
-    B.tri_norm_bwd(x2, codes, exps, kind, stats, _param(weight), dy2, None if dx is None else _rows(dx), dw, db, ws)
+        C = dy.shape[-1]
+        dw, db = dy.new_empty((2, C), dtype=torch.float32).unbind(0)
+        ws = dy.new_empty(B.tri_norm_bwd_workspace_bytes(dy.numel() // C, C), dtype=torch.uint8)
+    if isinstance(x, Act8):
+        B.tri_norm_bwd(None, _rows(x.codes), _rows(x.exps), x.kind, stats, _param(weight), _rows(dy), dx, dw, db, ws)
+    else:
+        B.tri_norm_bwd(_rows(x), None, None, 0, stats, _param(weight), _rows(dy), dx, dw, db, ws)
     return dx, dw, db
 
 
@@ -201,7 +202,7 @@ class NormLinearFunction(torch.autograd.Function):
                 y = norm_restore(x, stats, weight, bias, proj.dtype)
             else:
                 y = norm_forward(x, weight, bias, ctx.eps, proj.dtype)[0]
-            dproj = torch.matmul(g.reshape(-1, g.shape[-1]).t(), _rows(y))
+            dproj = torch.matmul(g.reshape(-1, g.shape[-1]).t(), y.view(-1, y.shape[-1]))
         if need[0] or need[1] or need[2]:
             dx, dw, db = norm_backward(x, stats, torch.matmul(g, proj), weight, need[0], need[1] or need[2])
         return (dx, _like(dw, weight) if need[1] else None, _like(db, bias) if need[2] else None, dproj, None, None)

@@ -53,21 +53,28 @@ def relpos_edges_log(per_side: int, max_distance: int, device="cuda") -> torch.T
 def _layout(t: torch.Tensor) -> torch.Tensor:
     """t itself if the C ABI accepts its layout (unit inner stride, the others non-negative
     multiples of 8, 16-byte aligned data), else a copy with rows padded to a multiple of 8."""
+    if t.is_contiguous() and t.shape[3] % 8 == 0 and t.data_ptr() % 16 == 0:
+        return t
     ok = (t.shape[3] == 1 or t.stride(3) == 1) and t.data_ptr() % 16 == 0
     if ok and all(n == 1 or (s >= 0 and s % 8 == 0) for n, s in zip(t.shape[:3], t.stride()[:3])):
         return t
-    return _padded(t.shape, t.device).copy_(t)
+    return _padded(t.shape, t).copy_(t)
 
 
-def _padded(shape, device) -> torch.Tensor:
+def _padded(shape, like) -> torch.Tensor:
     *lead, n = shape
-    return torch.empty((*lead, (n + 7) // 8 * 8), dtype=torch.bfloat16, device=device)[..., :n]
+    if n % 8 == 0:
+        return like.new_empty(shape, dtype=torch.bfloat16)
+    return like.new_empty((*lead, (n + 7) // 8 * 8), dtype=torch.bfloat16)[..., :n]
 
 
 def _index(pos_q, pos_k, group_q, group_k, like=None):
     """Positions and groups as int32 [B, N], one batch size (that of ``like`` where all are shared),
     groups laid out as the positions."""
     ts = [pos_q, pos_k, group_q, group_k]
+    if all(t is None or (t.dim() == 2 and t.is_contiguous()) for t in ts) and pos_q.shape[0] == pos_k.shape[0] and (
+            like is None or like.shape[0] == pos_q.shape[0]):
+        return pos_q, pos_k, group_q, group_k  # checked where they are used
     for t in ts:
         if t is not None and (t.dtype != torch.int32 or not 1 <= t.dim() <= 2):
             raise B.TriAttnError(B.TRI_ATTN_ERR_DTYPE, f"positions and groups are int32 [N] or [B, N], got {t.dtype} {list(t.shape)}")
@@ -92,7 +99,7 @@ def relpos_forward(table, edges, pos_q, pos_k, group_q=None, group_k=None, base=
     """The bias, BF16 [B, H, Nq, Nk] with rows padded to a multiple of 8 elements.  table BF16 or
     FP32 [buckets, H]; positions and groups int32 [N] or [B, N]; base BF16 [B, H, Nq, Nk]."""
     q, k, gq, gk = _index(pos_q, pos_k, group_q, group_k, base)
-    bias = _padded((q.shape[0], table.shape[1], q.shape[1], k.shape[1]), table.device)
+    bias = _padded((q.shape[0], table.shape[1], q.shape[1], k.shape[1]), table)
     B.tri_relpos_fwd(table.contiguous(), edges, q, k, gq, gk, None if base is None else _layout(base), bias)
     return bias
 
@@ -101,9 +108,9 @@ def relpos_backward(dbias, edges, pos_q, pos_k, group_q=None, group_k=None):
     """The table's gradient, FP32 [buckets, H], for the bias's gradient (BF16 [B, H, Nq, Nk])."""
     q, k, gq, gk = _index(pos_q, pos_k, group_q, group_k, dbias)
     E, H = edges.shape[0], dbias.shape[1]
-    dtable = torch.empty((E + 1 + (gq is not None), H), dtype=torch.float32, device=dbias.device)
-    need = B.tri_relpos_bwd_workspace_bytes(q.shape[0], H, q.shape[1], k.shape[1], E, gq is not None)
-    ws = torch.empty(need, dtype=torch.uint8, device=dbias.device)
+    dtable = dbias.new_empty((E + 1 + (gq is not None), H), dtype=torch.float32)
+    ws = dbias.new_empty(B.tri_relpos_bwd_workspace_bytes(q.shape[0], H, q.shape[1], k.shape[1], E, gq is not None),
+                         dtype=torch.uint8)
     B.tri_relpos_bwd(_layout(dbias), edges, q, k, gq, gk, dtable, ws)
     return dtable
 
