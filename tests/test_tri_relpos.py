@@ -109,7 +109,7 @@ def test_workspace_bytes(lib):
     assert lib.tri_relpos_fwd(None, None) == lib.tri_relpos_bwd(None, None) == Bd.TRI_ATTN_ERR_NULL
     assert ws(1, 4, 64, 64, 0, False) == ws(1, 0, 64, 64, 8, False) == ws(0, 4, 64, 64, 8, False) == 0
     for B, H, N, E in ((1, 4, 768, 64), (2, 12, 1031, 39), (1, 1, 1, 1), (1, 40, 2048, 510), (3, 4096, 5, 510)):
-        assert 0 < ws(B, H, N, N, E, False) <= ws(B, H, N, N, E, True) <= 148 * 6 * (E + 2) * H * 4
+        assert 0 < ws(B, H, N, N, E, False) <= ws(B, H, N, N, E, True) <= 148 * 8 * (E + 2) * H * 4
 
 
 def test_edges_helpers():

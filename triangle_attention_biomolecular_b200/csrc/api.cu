@@ -142,8 +142,10 @@ tri_attn_status ensure_device() {
                                tri::TriGateLayout::SMEM) == cudaSuccess;
     ok &= cudaFuncSetAttribute(tri::tri_gate_bwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                tri::TriGateBwdLayout::SMEM) == cudaSuccess;
-    ok &= cudaFuncSetAttribute(tri::tri_relpos_bwd_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024) ==
-          cudaSuccess;
+    ok &= cudaFuncSetAttribute(tri::tri_relpos_bwd_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               tri::kRelBwdSmem) == cudaSuccess;
+    ok &= cudaFuncSetAttribute(tri::tri_relpos_bwd_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               tri::kRelBwdSmem) == cudaSuccess;
     if (!ok || !encoder()) {
         cudaGetLastError();
         return TRI_ATTN_ERR_CUDA;

@@ -250,13 +250,13 @@ RelposBwdShape relpos_bwd_shape(int B, int H, int Nq, int Nk, int nb) {
     const int S = 32 / s.heads;
     const int64_t tiles = static_cast<int64_t>(B) * ((chunks + S - 1) / S);
     s.warps = tri::kRelBwdWarps;
-    while (s.warps > 1 && tri::relpos_bwd_smem(nb, s.warps) > 200 * 1024) --s.warps;
+    while (s.warps > 1 && tri::relpos_bwd_smem(nb, s.warps) > tri::kRelBwdSmem) --s.warps;
     s.smem = tri::relpos_bwd_smem(nb, s.warps);
     // as many tasks as warps run at once, each with at least one batch of rows
-    const int64_t want = std::max<int64_t>(1, 148 * 20 / (tiles * s.head_blocks));
+    const int64_t want = std::max<int64_t>(1, 148 * tri::kRelBwdBlocks * s.warps / (tiles * s.head_blocks));
     s.row_tasks = static_cast<int>(std::min<int64_t>(want, (Nq + tri::kRelRows - 1) / tri::kRelRows));
     const int64_t tasks = tiles * s.row_tasks;
-    s.grid = static_cast<unsigned>(std::min<int64_t>((tasks + s.warps - 1) / s.warps, 148 * 5));
+    s.grid = static_cast<unsigned>(std::min<int64_t>((tasks + s.warps - 1) / s.warps, 148 * tri::kRelBwdBlocks));
     return s;
 }
 
@@ -404,7 +404,9 @@ tri_attn_status tri_relpos_bwd(const tri_relpos_bwd_args* a, tri_attn_stream_t s
     p.dbias = static_cast<const __nv_bfloat16*>(a->dbias.ptr);
     for (int x = 0; x < 3; ++x) p.ds[x] = a->dbias.stride[x];
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    tri::tri_relpos_bwd_kernel<<<dim3(s.grid, s.head_blocks), s.warps * 32, s.smem, cs>>>(p);
+    with_bool(p.grp_q != nullptr, [&](auto v) {
+        tri::tri_relpos_bwd_kernel<decltype(v)::value><<<dim3(s.grid, s.head_blocks), s.warps * 32, s.smem, cs>>>(p);
+    });
     const int n = p.nb * f.H;
     tri::tri_ordered_sum_kernel<<<(n + 31) / 32, 1024, 0, cs>>>(p.partial, static_cast<int>(s.grid), n, a->dtable, n,
                                                                nullptr);

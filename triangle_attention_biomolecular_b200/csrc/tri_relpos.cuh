@@ -33,7 +33,7 @@ struct RelposParams {
     int64_t os[3];
     const __nv_bfloat16* dbias;
     int64_t ds[3];
-    int row_tasks;                 // backward: warps that share the rows of a column tile
+    int row_tasks;                 // backward: warps that share the rows of a column tile, batch by batch
     float* partial;                // backward: [gridDim.x][nb][H]
 };
 
@@ -42,19 +42,21 @@ struct RelposParams {
 // are looked up: all there are (others are clamped to the ends) when the edges
 // lie that close together, else the kRelLut around 0, and those outside are
 // searched.
+// number of edges <= d
+__device__ __forceinline__ int relpos_search(const int32_t* edges, int E, int d) {
+    int n = 0;
+#pragma unroll 1
+    for (int s = 256; s > 0; s >>= 1)
+        if (n + s <= E && edges[n + s - 1] <= d) n += s;
+    return n;
+}
+
 struct RelposBuckets {
     const int32_t* edges;
     const uint16_t* lut;
     int E, lo, size, dmin, dmax;
 
-    // number of edges <= d; rarely needed, so one copy of the code
-    __device__ __noinline__ int search(int d) const {
-        int n = 0;
-#pragma unroll 1
-        for (int s = 256; s > 0; s >>= 1)
-            if (n + s <= E && edges[n + s - 1] <= d) n += s;
-        return n;
-    }
+    __device__ __forceinline__ int search(int d) const { return relpos_search(edges, E, d); }
     __device__ __forceinline__ void init(int32_t* sh_edges, uint16_t* sh_lut, const RelposParams& p) {
         for (int e = threadIdx.x; e < p.E; e += blockDim.x) sh_edges[e] = p.edges[e];
         __syncthreads();
@@ -87,26 +89,25 @@ struct RelposBuckets {
         const uint32_t x = static_cast<uint32_t>(d) - static_cast<uint32_t>(lo);
         return x < static_cast<uint32_t>(size) ? lut[x] : search(d);
     }
-    // eight at once, their look-ups in flight together
-    __device__ __forceinline__ void of8(const int (&d)[8], int (&k)[8]) const {
+    // eight distances into their buckets, the look-ups in flight together
+    __device__ __forceinline__ void of8(int (&k)[8]) const {
         bool far[8], any = false;
+        int near[8];
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
-            const int dx = min(max(d[x], dmin), dmax);
-            const uint32_t at = static_cast<uint32_t>(dx) - static_cast<uint32_t>(lo);
+            const uint32_t at = static_cast<uint32_t>(min(max(k[x], dmin), dmax)) - static_cast<uint32_t>(lo);
             far[x] = at >= static_cast<uint32_t>(size);
             any |= far[x];
-            k[x] = lut[far[x] ? 0u : at];
+            near[x] = lut[far[x] ? 0u : at];
         }
         if (any) {
 #pragma unroll
             for (int x = 0; x < 8; ++x)
-                if (far[x]) k[x] = search(d[x]);
+                if (far[x]) near[x] = search(k[x]);
         }
+#pragma unroll
+        for (int x = 0; x < 8; ++x) k[x] = near[x];
     }
-    // the distances of bucket k are least(k) <= d <= most(k)
-    __device__ __forceinline__ int least(int k) const { return k > 0 ? edges[k - 1] : INT32_MIN; }
-    __device__ __forceinline__ int most(int k) const { return k < E ? edges[k] - 1 : INT32_MAX; }
 };
 
 constexpr int kRelThreads = 256;
@@ -171,12 +172,11 @@ __global__ void __launch_bounds__(kRelThreads) tri_relpos_fwd_kernel(const __gri
 #pragma unroll
             for (int x = 0; x < 8; ++x) at[x] = first * pitch;
         } else {
-            int k[8];
 #pragma unroll
             for (int x = 0; x < 8; ++x) key[x] = RelposBuckets::distance(key[x], pq);
-            bucket.of8(key, k);
+            bucket.of8(key);
 #pragma unroll
-            for (int x = 0; x < 8; ++x) at[x] = (at[x] ? p.E + 1 : k[x]) * pitch;
+            for (int x = 0; x < 8; ++x) at[x] = (at[x] ? p.E + 1 : key[x]) * pitch;
         }
         __nv_bfloat16* out = p.bias + b * p.os[0] + h0 * p.os[1] + i * p.os[2] + j0;
         const __nv_bfloat16* in = BASE ? p.base + b * p.bs[0] + h0 * p.bs[1] + i * p.bs[2] + j0 : nullptr;
@@ -222,64 +222,77 @@ __global__ void __launch_bounds__(kRelThreads) tri_relpos_fwd_kernel(const __gri
 // (nor, 32 lanes to 32 banks, in a bank), so there are no atomics and every sum
 // has one order.
 //
-// Most chunks lie in one bucket as a whole (beyond the clipping distance, or in
-// another group) or across one edge.  A lane therefore holds two neighbouring
-// buckets in hand, each with a sum in a register, and the bounds that tell with two
-// comparisons that a chunk lies within them; they are put down into the column
-// when a chunk does not.  Rows are taken kRelRows at a time, so that their loads
-// are in flight together; the few rows that need more than the registers are read
-// again afterwards (from the cache) by one compact loop: unrolled into the walk,
-// that code did not fit the instruction cache.  A task's batches of rows lie a
-// whole round of tasks apart, since the rows near the diagonal cost the most.
-constexpr int kRelBwdWarps = 4;
-constexpr int kRelRows = 8;
+// Most chunks lie in one bucket as a whole: beyond the first or the last edge, in
+// another group, or between two edges far apart.  A lane therefore keeps five sums
+// in registers, those of the first and the last bucket, of the pairs of different
+// groups, and of two neighbouring buckets it has in hand, and only a chunk that
+// none of them covers takes the slow way: its buckets are looked up key by key, and
+// either become the two in hand or are added to the column.  kRelRows rows are
+// taken at a time, their loads in flight together; where one sum takes them all they
+// cost some 25 instructions a row, else they are gone through one by one (and read
+// again, from the cache) by a loop of their own, since unrolled into the walk that
+// code did not fit the instruction cache.
+constexpr int kRelBwdWarps = 8, kRelBwdBlocks = 2;  // per block, blocks per SM
+constexpr int kRelRows = 4;
+constexpr int kRelBwdSmem = 200 * 1024;  // the columns of as many warps as fit
 
 __host__ constexpr size_t relpos_bwd_smem(int nb, int warps) {
     return static_cast<size_t>(warps) * nb * 32 * 4 + 512 * 4 + kRelLut * 2;
 }
 
-// the two buckets a lane has in hand: first and, if there is one, first + 1
+__device__ __forceinline__ int relpos_cut(int64_t v) {
+    return static_cast<int>(v < INT32_MIN ? INT32_MIN : v > INT32_MAX ? INT32_MAX : v);
+}
+
+// The two buckets a lane has in hand, first and first + 1 (first < E).  What they
+// mean for the chunk's keys is kept in terms of the query's position q, so that a
+// row costs comparisons and no saturating subtraction: the chunk lies within the
+// two for qlo < q < qhi, and key x of it above the edge between them for q < t[x]
+// (tmin .. tmax).
+// Bounds past 32 bits are cut to positions that then lie outside.
 struct RelposPair {
-    int first, least, edge, most;  // distances least .. edge - 1 and edge .. most
+    int first, qlo, qhi, tmin, tmax, t[8];
     float sum0, sum1;
-    __device__ __forceinline__ void take(const RelposBuckets& bucket, int k) {
+    // n keys at positions pk, from their least to their greatest one
+    __device__ __forceinline__ void take(const RelposBuckets& bucket, int k, const int32_t* pk, int n, int pmin,
+                                         int pmax) {
         first = k;
-        least = bucket.least(k);
-        edge = k < bucket.E ? bucket.edges[k] : INT32_MAX;
-        most = bucket.most(min(k + 1, bucket.E));
         sum0 = sum1 = 0.f;
+        asm volatile("" : "+l"(pk));  // keeps eight loop-invariant addresses out of the walk's registers
+#pragma unroll
+        for (int x = 0; x < 8; ++x)
+            t[x] = relpos_cut(static_cast<int64_t>(pk[min(x, n - 1)]) - bucket.edges[k] + 1);
+        tmin = relpos_cut(static_cast<int64_t>(pmin) - bucket.edges[k] + 1);
+        tmax = relpos_cut(static_cast<int64_t>(pmax) - bucket.edges[k] + 1);
+        qhi = k > 0 ? relpos_cut(static_cast<int64_t>(pmin) - bucket.edges[k - 1] + 1) : INT32_MAX;
+        qlo = k + 1 < bucket.E ? relpos_cut(static_cast<int64_t>(pmax) - bucket.edges[k + 1]) : INT32_MIN;
     }
-    __device__ __forceinline__ void put(float* column, int E) const {
-        if (first < E) {
-            column[first * 32] += sum0;
-            column[(first + 1) * 32] += sum1;
-        } else {
-            column[E * 32] += sum0 + sum1;
-        }
-    }
-    // a chunk across the edge
-    __device__ __forceinline__ void split(const float (&v)[8], const int (&pk)[8], int pq) {
+    __device__ __forceinline__ bool fits(int q) const { return q > qlo && q < qhi; }
+    __device__ __forceinline__ void add(const float (&v)[8], int q) {
         float a = 0.f, b = 0.f;
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
-            const bool up = RelposBuckets::distance(pk[x], pq) >= edge;
-            a += up ? 0.f : v[x];
-            b += up ? v[x] : 0.f;
+            if (q < t[x])
+                b += v[x];
+            else
+                a += v[x];
         }
         sum0 += a;
         sum1 += b;
     }
+    __device__ __forceinline__ void put(float* column) const {
+        column[first * 32] += sum0;
+        column[(first + 1) * 32] += sum1;
+    }
 };
 
-__device__ __forceinline__ void relpos_load8(const __nv_bfloat16* s, int n, uint4& w) {
-    if (n == 8) {
-        w = *reinterpret_cast<const uint4*>(s);
-    } else {
-        uint32_t v[8];
+// eight keys of a row, of which n exist (n < 8 only at the end of a row)
+__device__ __forceinline__ uint4 relpos_load8(const __nv_bfloat16* s, int n) {
+    if (n == 8) return *reinterpret_cast<const uint4*>(s);
+    uint32_t v[8];
 #pragma unroll
-        for (int x = 0; x < 8; ++x) v[x] = x < n ? __bfloat16_as_ushort(s[x]) : 0u;
-        w = make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
-    }
+    for (int x = 0; x < 8; ++x) v[x] = x < n ? __bfloat16_as_ushort(s[x]) : 0u;
+    return make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
 }
 __device__ __forceinline__ void relpos_values(const uint4& w, float (&v)[8]) {
     v[0] = bf16lo(w.x); v[1] = bf16hi(w.x);
@@ -287,7 +300,6 @@ __device__ __forceinline__ void relpos_values(const uint4& w, float (&v)[8]) {
     v[4] = bf16lo(w.z); v[5] = bf16hi(w.z);
     v[6] = bf16lo(w.w); v[7] = bf16hi(w.w);
 }
-
 __device__ __forceinline__ float relpos_sum8(const float (&v)[8]) {
     const float2 a = fadd2(make_float2(v[0], v[1]), make_float2(v[2], v[3]));
     const float2 b = fadd2(make_float2(v[4], v[5]), make_float2(v[6], v[7]));
@@ -295,7 +307,24 @@ __device__ __forceinline__ float relpos_sum8(const float (&v)[8]) {
     return c.x + c.y;
 }
 
-__global__ void __launch_bounds__(kRelBwdWarps * 32, 5) tri_relpos_bwd_kernel(const __grid_constant__ RelposParams p) {
+// kRelRows rows of a lane's chunk, as loaded
+struct RelposBatch {
+    uint4 w[kRelRows];
+    int q[kRelRows], g[kRelRows];
+    template <bool GROUPS>
+    __device__ __forceinline__ void load(const __nv_bfloat16* s, int64_t step, int nj, const int32_t* pos,
+                                         const int32_t* grp) {
+#pragma unroll
+        for (int u = 0; u < kRelRows; ++u, s += step) {
+            w[u] = relpos_load8(s, nj);
+            q[u] = pos[u];
+            g[u] = GROUPS ? grp[u] : 0;
+        }
+    }
+};
+
+template <bool GROUPS>
+__global__ void __launch_bounds__(kRelBwdWarps * 32, kRelBwdBlocks) tri_relpos_bwd_kernel(const __grid_constant__ RelposParams p) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const bool dead = device_error_pending();
     const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -312,103 +341,124 @@ __global__ void __launch_bounds__(kRelBwdWarps * 32, 5) tri_relpos_bwd_kernel(co
     const int tiles = (p.chunks + S - 1) / S;
     float* mine = sums + static_cast<size_t>(warp) * p.nb * 32 + lane;
     const int64_t tasks = static_cast<int64_t>(p.B) * tiles * p.row_tasks;
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * warps + warp; t < tasks;
-         t += static_cast<int64_t>(gridDim.x) * warps) {
-        const int rt = static_cast<int>(t % p.row_tasks);
-        const int64_t bt = t / p.row_tasks;
-        const int tile = static_cast<int>(bt % tiles), b = static_cast<int>(bt / tiles);
+    for (int64_t task = static_cast<int64_t>(blockIdx.x) * warps + warp; task < tasks;
+         task += static_cast<int64_t>(gridDim.x) * warps) {
+        // neighbouring warps take neighbouring keys of the same rows
+        const int tile = static_cast<int>(task % tiles);
+        const int64_t br = task / tiles;
+        const int rt = static_cast<int>(br % p.row_tasks), b = static_cast<int>(br / p.row_tasks);
         const int c = tile * S + sub;
         if (c >= p.chunks || h >= p.H) continue;  // no barrier or warp-wide step inside the walk
         const int j0 = c * 8, nj = min(8, p.Nk - j0);
-        int pk[8], gk[8], pmin = INT32_MAX, pmax = INT32_MIN;
+        const int32_t* keys = p.pos_k + b * p.ks + j0;
+        const int32_t* gkeys = GROUPS ? p.grp_k + b * p.ks + j0 : nullptr;
+        const int32_t* pos = p.pos_q + b * p.qs;
+        const int32_t* grp = GROUPS ? p.grp_q + b * p.qs : nullptr;
+        const int g0 = GROUPS ? gkeys[0] : 0;
         bool one_group = true;
+        RelposPair hand;
+        int pmin = INT32_MAX, pmax = INT32_MIN;
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
-            const int xx = min(x, nj - 1);
-            pk[x] = p.pos_k[b * p.ks + j0 + xx];
-            gk[x] = p.grp_k ? p.grp_k[b * p.ks + j0 + xx] : 0;
-            pmin = min(pmin, pk[x]);
-            pmax = max(pmax, pk[x]);
-            one_group &= gk[x] == gk[0];
+            const int k = keys[min(x, nj - 1)];
+            pmin = min(pmin, k);
+            pmax = max(pmax, k);
+            if (GROUPS) one_group &= gkeys[min(x, nj - 1)] == g0;
         }
+        // all keys lie below the first edge for q > q0, above the last for q < qE
+        const int q0 = one_group ? relpos_cut(static_cast<int64_t>(pmax) - sh_edges[0]) : INT32_MAX;
+        const int qE = one_group ? relpos_cut(static_cast<int64_t>(pmin) - sh_edges[p.E - 1] + 1) : INT32_MIN;
+        hand.take(bucket, 0, keys, nj, pmin, pmax);
+        if (!one_group) hand.qhi = INT32_MIN;  // nothing fits
+        float low = 0.f, high = 0.f, apart = 0.f;
         const __nv_bfloat16* src = p.dbias + b * p.ds[0] + h * p.ds[1] + j0;
-        const int32_t* pos = p.pos_q + b * p.qs;
-        const int32_t* grp = p.grp_q ? p.grp_q + b * p.qs : nullptr;
-        RelposPair hand;
-        hand.take(bucket, 0);
-        float apart = 0.f;  // pairs of different groups
-        for (int i0 = rt * kRelRows; i0 < p.Nq; i0 += p.row_tasks * kRelRows) {
-            uint4 w[kRelRows];
-            int pq[kRelRows], gq[kRelRows];
-            const __nv_bfloat16* s = src + i0 * p.ds[2];
-            const int rows = min(kRelRows, p.Nq - i0);
-            if (rows == kRelRows) {
+        const int64_t step = p.ds[2];
+        // a batch of rows, loaded while the one before it is added up
+        RelposBatch next;
+        const int stride = p.row_tasks * kRelRows;
+        int i0 = rt * kRelRows;
+        if (i0 + kRelRows <= p.Nq) next.load<GROUPS>(src + i0 * step, step, nj, pos + i0, grp + i0);
+        for (; i0 < p.Nq; i0 += stride) {
+            if (i0 + kRelRows <= p.Nq) {
+                const RelposBatch now = next;
+                const int i2 = i0 + stride;
+                if (i2 + kRelRows <= p.Nq) next.load<GROUPS>(src + i2 * step, step, nj, pos + i2, grp + i2);
+                int lo = now.q[0], hi = now.q[0];
+                bool same = one_group, other = GROUPS && one_group;
 #pragma unroll
-                for (int u = 0; u < kRelRows; ++u, s += p.ds[2]) {
-                    pq[u] = pos[i0 + u];
-                    gq[u] = grp ? grp[i0 + u] : 0;
-                    relpos_load8(s, nj, w[u]);
-                }
-            } else {
-#pragma unroll
-                for (int u = 0; u < kRelRows; ++u, s += p.ds[2]) {
-                    pq[u] = gq[u] = 0;
-                    if (u < rows) {
-                        pq[u] = pos[i0 + u];
-                        gq[u] = grp ? grp[i0 + u] : 0;
-                        relpos_load8(s, nj, w[u]);
+                for (int u = 0; u < kRelRows; ++u) {
+                    lo = min(lo, now.q[u]);
+                    hi = max(hi, now.q[u]);
+                    if (GROUPS) {
+                        same &= now.g[u] == g0;
+                        other &= now.g[u] != g0;
                     }
                 }
-            }
-            uint32_t more = 0;
+                const bool is_low = same && lo > q0, is_high = same && hi < qE;
+                const bool in = same && !is_low && !is_high && lo > hand.qlo && hi < hand.qhi;
+                const bool below = in && lo >= hand.tmax, above = in && hi < hand.tmin;
+                if (other || is_low || is_high || below || above) {
+                    float2 a[kRelRows];
 #pragma unroll
-            for (int u = 0; u < kRelRows; ++u) {
-                if (u >= rows) break;
-                const int lo = RelposBuckets::distance(pmin, pq[u]), hi = RelposBuckets::distance(pmax, pq[u]);
-                float v[8];
-                relpos_values(w[u], v);
-                const float all = relpos_sum8(v);
-                const bool other = one_group && gk[0] != gq[u];
-                const bool fits = one_group && !other && lo >= hand.least && hi <= hand.most;
-                const bool below = fits && hi < hand.edge, above = fits && lo >= hand.edge;
-                apart += other ? all : 0.f;
-                hand.sum0 += below ? all : 0.f;
-                hand.sum1 += above ? all : 0.f;
-                if (fits && !below && !above) hand.split(v, pk, pq[u]);
-                if (!other && !fits) more |= 1u << u;
+                    for (int u = 0; u < kRelRows; ++u)
+                        a[u] = fadd2(fadd2(bf16x2_to_f2(now.w[u].x), bf16x2_to_f2(now.w[u].y)),
+                                     fadd2(bf16x2_to_f2(now.w[u].z), bf16x2_to_f2(now.w[u].w)));
+#pragma unroll
+                    for (int m = 1; m < kRelRows; m *= 2)
+#pragma unroll
+                        for (int u = 0; u < kRelRows; u += 2 * m) a[u] = fadd2(a[u], a[u + m]);
+                    const float all = a[0].x + a[0].y;
+                    apart += other ? all : 0.f;
+                    low += is_low ? all : 0.f;
+                    high += is_high ? all : 0.f;
+                    hand.sum0 += below ? all : 0.f;
+                    hand.sum1 += above ? all : 0.f;
+                    continue;
+                }
             }
-            while (more) {
-                const int i = i0 + __ffs(more) - 1;
-                more &= more - 1;
-                uint4 wi;
+#pragma unroll 1
+            for (int i = i0; i < min(p.Nq, i0 + kRelRows); ++i) {
+                const int q = pos[i], g = GROUPS ? grp[i] : 0;
                 float v[8];
-                relpos_load8(src + i * p.ds[2], nj, wi);
-                relpos_values(wi, v);
-                const int q = pos[i], g = grp ? grp[i] : 0;
-                if (one_group) {  // and of the row's group
-                    const int lo = RelposBuckets::distance(pmin, q), hi = RelposBuckets::distance(pmax, q);
-                    if (lo < hand.least || hi > hand.most) {
-                        hand.put(mine, p.E);
-                        hand.take(bucket, bucket.of(lo));
-                    }
-                    if (hi <= hand.most) {
-                        hand.split(v, pk, q);
+                relpos_values(relpos_load8(src + i * step, nj), v);
+                if (one_group) {
+                    const float all = relpos_sum8(v);
+                    const bool other = GROUPS && g != g0;
+                    const bool is_low = !other && q > q0, is_high = !other && q < qE;
+                    apart += other ? all : 0.f;
+                    low += is_low ? all : 0.f;
+                    high += is_high ? all : 0.f;
+                    if (other || is_low || is_high) continue;
+                    if (hand.fits(q)) {
+                        hand.add(v, q);
                         continue;
                     }
                 }
-                // key by key; in ascending order of buckets (the usual case) equal neighbours are
-                // joined first, and what is left lies in different words
-                int d[8], k[8];
+                const int32_t* kp = keys;
+                asm volatile("" : "+l"(kp));  // keeps what depends on it from being held through the walk
+                int k[8], least = INT32_MAX, most = 0;
 #pragma unroll
-                for (int x = 0; x < 8; ++x) d[x] = RelposBuckets::distance(pk[x], q);
-                bucket.of8(d, k);
+                for (int x = 0; x < 8; ++x) k[x] = RelposBuckets::distance(kp[min(x, nj - 1)], q);
+                bucket.of8(k);
                 bool ascending = true;
 #pragma unroll
                 for (int x = 0; x < 8; ++x) {
-                    if (gk[x] != g) k[x] = p.E + 1;
+                    if (GROUPS && !one_group && gkeys[min(x, nj - 1)] != g) k[x] = p.E + 1;
                     if (x > 0) ascending &= k[x] >= k[x - 1];
+                    least = min(least, k[x]);
+                    most = max(most, k[x]);
                 }
-                if (ascending) {
+                if (one_group && most - least <= 1) {  // two others to take in hand
+                    hand.put(mine);
+                    hand.take(bucket, min(least, p.E - 1), keys, nj, pmin, pmax);
+#pragma unroll
+                    for (int x = 0; x < 8; ++x) {
+                        hand.sum0 += k[x] == hand.first ? v[x] : 0.f;
+                        hand.sum1 += k[x] == hand.first ? 0.f : v[x];
+                    }
+                } else if (ascending) {
+                    // the usual case: equal neighbours are joined first, and what is left lies in
+                    // different words
                     float old[8];
 #pragma unroll
                     for (int x = 0; x < 8; ++x) {
@@ -428,18 +478,30 @@ __global__ void __launch_bounds__(kRelBwdWarps * 32, 5) tri_relpos_bwd_kernel(co
                 }
             }
         }
-        hand.put(mine, p.E);
-        if (p.grp_k) mine[(p.E + 1) * 32] += apart;
+        hand.put(mine);
+        mine[0] += low;
+        mine[p.E * 32] += high;
+        if (GROUPS) mine[(p.E + 1) * 32] += apart;
     }
     __syncthreads();
     // the block's sums: a warp per bucket, over the warps, then over the chunks side by side
     float* out = p.partial + static_cast<int64_t>(blockIdx.x) * p.nb * p.H;
 #pragma unroll 4
     for (int k = warp; k < p.nb; k += warps) {
-        float s = 0.f;
-        for (int w = 0; w < warps; ++w) s += sums[(static_cast<size_t>(w) * p.nb + k) * 32 + lane];
-        for (int m = 1; m < S; m <<= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, m);
-        if (sub == 0 && h < p.H && !dead) out[static_cast<int64_t>(k) * p.H + h] = s;
+        float s[kRelBwdWarps];
+#pragma unroll
+        for (int w = 0; w < kRelBwdWarps; ++w)
+            s[w] = w < warps ? sums[(static_cast<size_t>(w) * p.nb + k) * 32 + lane] : 0.f;
+#pragma unroll
+        for (int m = 1; m < kRelBwdWarps; m *= 2)
+#pragma unroll
+            for (int w = 0; w < kRelBwdWarps; w += 2 * m) s[w] += s[w + m];
+#pragma unroll
+        for (int m = 1; m < 32; m *= 2) {
+            const float other = __shfl_xor_sync(0xFFFFFFFFu, s[0], m);
+            if (m < S) s[0] += other;
+        }
+        if (sub == 0 && h < p.H && !dead) out[static_cast<int64_t>(k) * p.H + h] = s[0];
     }
 }
 
