@@ -38,28 +38,27 @@ struct NormShape {
     int lanes, threads;
     int64_t per_block;
 };
-NormShape norm_shape(int C) {
+NormShape norm_shape(int C, bool vec) {
     const int units = (C + 15) / 16;
     NormShape s{};
-    if (units <= 32) {
-        s.lanes = 1;
-        while (s.lanes < units) s.lanes *= 2;
-        s.threads = tri::kNormThreads;
-    } else {
-        s.lanes = (units + 31) / 32 * 32;
-        s.threads = s.lanes;
-    }
+    s.threads = tri::kNormThreads;
+    if (units > 32)
+        s.lanes = s.threads = (units + 31) / 32 * 32;
+    else if (!vec)
+        s.lanes = units <= 4 ? tri::kBy4 : tri::kBy32;
+    else
+        for (s.lanes = 1; s.lanes < units;) s.lanes *= 2;
     s.per_block = s.threads / s.lanes;
     return s;
 }
-// blocks of the backward: a function of the sizes alone, like every order of additions there
-int64_t norm_bwd_blocks(int64_t R, int C) {
-    const NormShape s = norm_shape(C);
-    return std::min<int64_t>((R + s.per_block - 1) / s.per_block, 148 * (s.lanes > 32 ? 4 : 2));
+// blocks of the backward: a function of the sizes and the alignment alone, like every order of
+// additions there
+int64_t norm_bwd_blocks(int64_t R, int C, bool vec) {
+    const NormShape s = norm_shape(C, vec);
+    return std::min<int64_t>((R + s.per_block - 1) / s.per_block, 148 * (s.lanes > 32 ? 4 : tri::kNormBwdBlocks));
 }
 
-void norm_params(NormParams& p, const tri_norm_fwd_args& a) {
-    const NormShape s = norm_shape(a.C);
+void norm_params(NormParams& p, const tri_norm_fwd_args& a, const NormShape& s) {
     p.R = a.R;
     p.C = a.C;
     p.lanes = s.lanes;
@@ -101,6 +100,17 @@ void with_bool(bool v, F&& f) {
     v ? f(std::true_type{}) : f(std::false_type{});
 }
 
+// f(how the lanes share a row, whether a row takes a whole block)
+template <typename F>
+void with_mode(bool vec, int lanes, F&& f) {
+    if (lanes > 32)
+        vec ? f(Int<tri::kVec>{}, std::true_type{}) : f(Int<tri::kBy32>{}, std::true_type{});
+    else if (vec)
+        f(Int<tri::kVec>{}, std::false_type{});
+    else
+        lanes == tri::kBy4 ? f(Int<tri::kBy4>{}, std::false_type{}) : f(Int<tri::kBy32>{}, std::false_type{});
+}
+
 tri_attn_status launched() { return cudaGetLastError() == cudaSuccess ? TRI_ATTN_OK : TRI_ATTN_ERR_CUDA; }
 
 tri_attn_status norm_fwd_impl(const tri_norm_fwd_args* a, bool restore, tri_attn_stream_t stream) {
@@ -119,28 +129,30 @@ tri_attn_status norm_fwd_impl(const tri_norm_fwd_args* a, bool restore, tri_attn
     if (act && (st = check_act8(a->act, a->R, a->C, !restore))) return st;
     if ((st = ensure_device())) return st;
     if (a->R == 0) return TRI_ATTN_OK;
-    NormParams p{};
-    norm_params(p, *a);
-    const NormShape s = norm_shape(a->C);
     const bool vec = a->C % 16 == 0 && vec_rows(a->y, a->y_stride, ye) && (!act || vec_act8(a->act)) &&
                      (restore || vec_rows(a->x, a->x_stride, xe));
-    const unsigned grid = static_cast<unsigned>(std::min<int64_t>((a->R + s.per_block - 1) / s.per_block, 148 * 8));
+    const NormShape s = norm_shape(a->C, vec);
+    NormParams p{};
+    norm_params(p, *a, s);
+    const unsigned grid = static_cast<unsigned>(
+        std::min<int64_t>((a->R + s.per_block - 1) / s.per_block, 148 * (s.lanes > 32 ? 8 : vec ? tri::kNormFwdBlocks : tri::kNormFwdBlocksBy)));
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    with_bool(vec, [&](auto v) {
-        constexpr bool VEC = decltype(v)::value;
+    with_mode(vec, s.lanes, [&](auto m, auto wd) {
+        constexpr int MODE = decltype(m)::value;
+        constexpr bool WIDE = decltype(wd)::value;
         with_types(restore ? a->y_type : a->x_type, a->y_type, [&](auto tx, auto ty) {
             using TX = decltype(tx);
             using TY = decltype(ty);
             if (restore) {
                 if constexpr (std::is_same<TX, TY>::value)
                     with_kind(a->act.kind, [&](auto k) {
-                        tri::tri_norm_fwd_kernel<TX, TY, decltype(k)::value, VEC, true><<<grid, s.threads, 0, cs>>>(p);
+                        tri::tri_norm_fwd_kernel<TX, TY, decltype(k)::value, MODE, true, WIDE><<<grid, s.threads, 0, cs>>>(p);
                     });
             } else if (!act) {
-                tri::tri_norm_fwd_kernel<TX, TY, tri::ACT_NONE, VEC, false><<<grid, s.threads, 0, cs>>>(p);
+                tri::tri_norm_fwd_kernel<TX, TY, tri::ACT_NONE, MODE, false, WIDE><<<grid, s.threads, 0, cs>>>(p);
             } else {
                 with_kind(a->act.kind, [&](auto k) {
-                    tri::tri_norm_fwd_kernel<TX, TY, decltype(k)::value, VEC, false><<<grid, s.threads, 0, cs>>>(p);
+                    tri::tri_norm_fwd_kernel<TX, TY, decltype(k)::value, MODE, false, WIDE><<<grid, s.threads, 0, cs>>>(p);
                 });
             }
         });
@@ -275,7 +287,8 @@ tri_attn_status tri_norm_restore(const tri_norm_fwd_args* a, tri_attn_stream_t s
 size_t tri_norm_bwd_workspace_bytes(int64_t R, int C) {
     if (check_norm_sizes(R, C)) return 0;
     // never 0 for sizes that are valid
-    return static_cast<size_t>(std::max<int64_t>(1, norm_bwd_blocks(R, C))) * 2 * C * sizeof(float);
+    const int64_t blocks = std::max(norm_bwd_blocks(R, C, false), norm_bwd_blocks(R, C, true));
+    return static_cast<size_t>(std::max<int64_t>(1, blocks)) * 2 * C * sizeof(float);
 }
 
 tri_attn_status tri_norm_bwd(const tri_norm_bwd_args* a, tri_attn_stream_t stream) {
@@ -300,31 +313,32 @@ tri_attn_status tri_norm_bwd(const tri_norm_bwd_args* a, tri_attn_stream_t strea
     }
     if ((st = ensure_device())) return st;
     if (!a->dx && !a->dw) return TRI_ATTN_OK;
+    const bool vec = f.C % 16 == 0 && vec_rows(a->dy, a->dy_stride, ye) &&
+                     (!a->dx || vec_rows(a->dx, a->dx_stride, xe)) &&
+                     (act ? vec_act8(f.act) : vec_rows(f.x, f.x_stride, xe));
+    const NormShape s = norm_shape(f.C, vec);
+    const int64_t blocks = norm_bwd_blocks(f.R, f.C, vec);
     NormParams p{};
-    norm_params(p, f);
+    norm_params(p, f, s);
     p.dy = a->dy;
     p.dys = a->dy_stride;
     p.dx = f.R ? a->dx : nullptr;
     p.dxs = a->dx_stride;
     p.partial = a->dw ? static_cast<float*>(a->workspace) : nullptr;
-    const NormShape s = norm_shape(f.C);
-    const int64_t blocks = norm_bwd_blocks(f.R, f.C);
-    const bool vec = f.C % 16 == 0 && vec_rows(a->dy, a->dy_stride, ye) &&
-                     (!a->dx || vec_rows(a->dx, a->dx_stride, xe)) &&
-                     (act ? vec_act8(f.act) : vec_rows(f.x, f.x_stride, xe));
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     if (blocks) {
-        with_bool(vec, [&](auto v) {
-            constexpr bool VEC = decltype(v)::value;
+        with_mode(vec, s.lanes, [&](auto m, auto wd) {
+            constexpr int MODE = decltype(m)::value;
+            constexpr bool WIDE = decltype(wd)::value;
             with_types(f.x_type, f.y_type, [&](auto tx, auto ty) {
                 using TX = decltype(tx);
                 using TY = decltype(ty);
                 const unsigned grid = static_cast<unsigned>(blocks);
                 if (!act)
-                    tri::tri_norm_bwd_kernel<TX, TY, tri::ACT_NONE, VEC><<<grid, s.threads, 0, cs>>>(p);
+                    tri::tri_norm_bwd_kernel<TX, TY, tri::ACT_NONE, MODE, WIDE><<<grid, s.threads, 0, cs>>>(p);
                 else
                     with_kind(f.act.kind, [&](auto k) {
-                        tri::tri_norm_bwd_kernel<TX, TY, decltype(k)::value, VEC><<<grid, s.threads, 0, cs>>>(p);
+                        tri::tri_norm_bwd_kernel<TX, TY, decltype(k)::value, MODE, WIDE><<<grid, s.threads, 0, cs>>>(p);
                     });
             });
         });

@@ -47,12 +47,17 @@ struct NormParams {
 // ---------------------------------------------------------------------------
 // sixteen channels of a row
 // ---------------------------------------------------------------------------
-// The channels lane g of a row's G lanes owns: 16 g .. 16 g + 15 when the row
-// can be moved in aligned vectors (VEC), else g, g + G, g + 2 G, ... so that
-// neighbouring lanes still touch neighbouring elements.
-template <bool VEC>
-__device__ __forceinline__ int norm_col(int g, int G, int k) {
-    return VEC ? g * 16 + k : g + G * k;
+// How the lanes of a row share its channels.  kVec: lane g has 16 g .. 16 g + 15,
+// moved in aligned vectors.  Rows that cannot be moved so are walked element by
+// element, neighbouring lanes on neighbouring channels, with a stride that the
+// compiler knows: by 4 lanes (up to 64 channels: 8 rows per warp) or by whole
+// warps, 512 channels each, where lane l has l, l + 32, l + 64, ...
+enum : int { kVec = 0, kBy4 = 4, kBy32 = 32 };
+template <int MODE>
+__device__ __forceinline__ int norm_col(int g, int k) {
+    if constexpr (MODE == kVec) return g * 16 + k;
+    if constexpr (MODE == kBy4) return g + 4 * k;
+    return (g >> 5) * 512 + (g & 31) + 32 * k;
 }
 
 __device__ __forceinline__ void ld_global_v8(const void* p, uint32_t* w) {
@@ -74,53 +79,63 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
     return __float2bfloat16_rn(v);
 }
 
-// channels that do not exist (past C, or of a row that does not exist) read as 0
-template <typename T, bool VEC>
-__device__ __forceinline__ void load16(const void* base, int64_t off, bool ok, int g, int G, int C, float (&v)[16]) {
-    const T* row = static_cast<const T*>(base) + off;
-    if constexpr (VEC) {
-        if (ok && g * 16 < C) {
-            if constexpr (sizeof(T) == 2) {
-                uint32_t w[8];
+// Sixteen channels as loaded, kept apart from their conversion so that a row can
+// be on its way while the one before it is worked on.  Channels that do not exist
+// (past C, or of a row that does not exist) read as 0.
+template <typename T, int MODE>
+struct NormRow {
+    uint32_t w[MODE == kVec && sizeof(T) == 2 ? 8 : 16];
+    __device__ __forceinline__ void load(const void* base, int64_t off, bool ok, int g, int G, int C) {
+        const T* row = static_cast<const T*>(base) + off;
+        if constexpr (MODE == kVec) {
+            if (ok && g * 16 < C) {
                 ld_global_v8(row + g * 16, w);
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    v[2 * k] = bf16lo(w[k]);
-                    v[2 * k + 1] = bf16hi(w[k]);
-                }
+                if constexpr (sizeof(T) == 4) ld_global_v8(row + g * 16 + 8, w + 8);
             } else {
-                uint32_t w[16];
-                ld_global_v8(row + g * 16, w);
-                ld_global_v8(row + g * 16 + 8, w + 8);
 #pragma unroll
-                for (int k = 0; k < 16; ++k) v[k] = __uint_as_float(w[k]);
+                for (uint32_t& x : w) x = 0u;
             }
         } else {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) v[k] = 0.f;
-        }
-    } else {
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            const int c = norm_col<VEC>(g, G, k);
-            v[k] = ok && c < C ? to_f32(row[c]) : 0.f;
+            for (int k = 0; k < 16; ++k) {
+                const int c = norm_col<MODE>(g, k);
+                w[k] = 0u;
+                if (ok && c < C) {
+                    if constexpr (sizeof(T) == 2)
+                        w[k] = static_cast<uint32_t>(__bfloat16_as_ushort(row[c])) << 16;
+                    else
+                        w[k] = __float_as_uint(row[c]);
+                }
+            }
         }
     }
-}
+    __device__ __forceinline__ void values(float2 (&v)[8]) const {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if constexpr (MODE == kVec && sizeof(T) == 2)
+                v[k] = bf16x2_to_f2(w[k]);
+            else
+                v[k] = make_float2(__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1]));
+        }
+    }
+};
 
-template <typename T, bool VEC>
-__device__ __forceinline__ void store16(void* base, int64_t off, bool ok, int g, int G, int C, const float (&v)[16]) {
+template <typename T, int MODE>
+__device__ __forceinline__ void store16(void* base, int64_t off, bool ok, int g, int G, int C, const float2 (&v)[8]) {
     T* row = static_cast<T*>(base) + off;
-    if constexpr (VEC) {
+    if constexpr (MODE == kVec) {
         if (ok && g * 16 < C) {
             uint32_t w[16];
             if constexpr (sizeof(T) == 2) {
 #pragma unroll
-                for (int k = 0; k < 8; ++k) w[k] = pack_bf16(v[2 * k], v[2 * k + 1]);
+                for (int k = 0; k < 8; ++k) w[k] = pack_bf16(v[k].x, v[k].y);
                 st_global_v8(row + g * 16, w);
             } else {
 #pragma unroll
-                for (int k = 0; k < 16; ++k) w[k] = __float_as_uint(v[k]);
+                for (int k = 0; k < 8; ++k) {
+                    w[2 * k] = __float_as_uint(v[k].x);
+                    w[2 * k + 1] = __float_as_uint(v[k].y);
+                }
                 st_global_v8(row + g * 16, w);
                 st_global_v8(row + g * 16 + 8, w + 8);
             }
@@ -128,24 +143,54 @@ __device__ __forceinline__ void store16(void* base, int64_t off, bool ok, int g,
     } else {
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-            const int c = norm_col<VEC>(g, G, k);
-            if (ok && c < C) row[c] = from_f32<T>(v[k]);
+            const int c = norm_col<MODE>(g, k);
+            if (ok && c < C) row[c] = from_f32<T>(k & 1 ? v[k / 2].y : v[k / 2].x);
         }
     }
 }
 
-// w or b for this lane's channels, `absent` where there is none
-template <bool VEC>
-__device__ __forceinline__ void load_param16(const void* p, int is_bf16, float absent, int g, int G, int C,
-                                             float (&v)[16]) {
-#pragma unroll
-    for (int k = 0; k < 16; ++k) {
-        const int c = norm_col<VEC>(g, G, k);
-        v[k] = absent;
-        if (p && c < C)
-            v[k] = is_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[c]) : static_cast<const float*>(p)[c];
-    }
+// w or b, `absent` where there is none: for a block's rows in shared memory, in
+// the order in which the lanes read it without bank conflicts (VEC: the q-th four
+// channels of lane g at 4 (q G + g), else channel c at c); for rows as wide as a
+// block, in the registers of the one thread that needs it
+__device__ __forceinline__ float norm_param(const void* p, int is_bf16, float absent, int c, int C) {
+    if (!p || c >= C) return absent;
+    return is_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[c]) : static_cast<const float*>(p)[c];
 }
+template <int MODE, bool WIDE>
+struct NormParam {
+    float2 own[WIDE ? 8 : 1];
+    const float* sh;
+    __device__ __forceinline__ void init(const void* p, int is_bf16, float absent, int g, int G, int C, float* shared) {
+        sh = shared;
+        if constexpr (WIDE) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                own[k] = make_float2(norm_param(p, is_bf16, absent, norm_col<MODE>(g, 2 * k), C),
+                                     norm_param(p, is_bf16, absent, norm_col<MODE>(g, 2 * k + 1), C));
+        } else {
+            for (int x = threadIdx.x; x < 16 * G; x += blockDim.x) {
+                const int lane = (x >> 2) & (G - 1), q = (x >> 2) / G;
+                shared[x] = norm_param(p, is_bf16, absent, MODE == kVec ? lane * 16 + q * 4 + (x & 3) : x, C);
+            }
+        }
+    }
+    // channels 4 q .. 4 q + 3 of this lane
+    __device__ __forceinline__ void get4(int q, int g, int G, float2& a, float2& b) const {
+        if constexpr (WIDE) {
+            a = own[2 * q];
+            b = own[2 * q + 1];
+        } else if constexpr (MODE == kVec) {
+            const float4 v = *reinterpret_cast<const float4*>(sh + 4 * (q * G + g));
+            a = make_float2(v.x, v.y);
+            b = make_float2(v.z, v.w);
+        } else {
+            const float* s = sh + norm_col<MODE>(g, 4 * q);
+            a = make_float2(s[0], s[MODE]);
+            b = make_float2(s[2 * MODE], s[3 * MODE]);
+        }
+    }
+};
 
 // ---------------------------------------------------------------------------
 // the 8-bit form
@@ -213,9 +258,15 @@ __device__ __forceinline__ void act8_value4(uint32_t w, float scale, float* v) {
 }
 
 // this lane's sixteen channels into the 8-bit form of their row; every lane of the warp calls it
-template <int ACT, bool VEC>
-__device__ __forceinline__ void act8_emit(const NormParams& p, int64_t row, bool ok, int g, int G, const float (&v)[16]) {
-    if constexpr (VEC) {
+template <int ACT, int MODE>
+__device__ __forceinline__ void act8_emit(const NormParams& p, int64_t row, bool ok, int g, int G, const float2 (&u)[8]) {
+    float v[16];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        v[2 * k] = u[k].x;
+        v[2 * k + 1] = u[k].y;
+    }
+    if constexpr (MODE == kVec) {
         uint32_t a = 0;
 #pragma unroll
         for (int k = 0; k < 16; ++k) a = max(a, __float_as_uint(v[k]) & 0x7FFFFFFFu);
@@ -235,23 +286,26 @@ __device__ __forceinline__ void act8_emit(const NormParams& p, int64_t row, bool
         }
     } else {
         uint32_t a[16];
-        const int per = G >= 32 ? 1 : 32 / G;  // consecutive k of one block
 #pragma unroll
         for (int k = 0; k < 16; ++k) a[k] = __float_as_uint(v[k]) & 0x7FFFFFFFu;
+        if constexpr (MODE == kBy32) {
 #pragma unroll
-        for (int s = 1; s < 16; s <<= 1)
-            if (s < per) {
+            for (int k = 0; k < 16; ++k)
+                if (32 * k < p.C) a[k] = __reduce_max_sync(0xFFFFFFFFu, a[k]);
+        } else {  // a block is eight k of four lanes
 #pragma unroll
-                for (int k = 0; k < 16; ++k)
-                    if ((k & s) == 0) a[k] = a[k + s] = max(a[k], a[k + s]);
+            for (int s = 0; s < 16; s += 8) {
+#pragma unroll
+                for (int k = 1; k < 8; ++k) a[s] = max(a[s], a[s + k]);
+                a[s] = max(a[s], __shfl_xor_sync(0xFFFFFFFFu, a[s], 1));
+                a[s] = max(a[s], __shfl_xor_sync(0xFFFFFFFFu, a[s], 2));
+#pragma unroll
+                for (int k = 1; k < 8; ++k) a[s + k] = a[s];
             }
-        for (int m = 1; m < 32 && m < G; m <<= 1) {
-#pragma unroll
-            for (int k = 0; k < 16; ++k) a[k] = max(a[k], __shfl_xor_sync(0xFFFFFFFFu, a[k], m));
         }
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-            const int c = norm_col<VEC>(g, G, k);
+            const int c = norm_col<MODE>(g, k);
             if (ok && c < p.C) {
                 const uint32_t eb = act8_exp<ACT>(a[k]);
                 const uint32_t code = eb == 255u ? 0u : act8_code2<ACT>(v[k], 0.f, act8_inv(eb));
@@ -262,30 +316,49 @@ __device__ __forceinline__ void act8_emit(const NormParams& p, int64_t row, bool
     }
 }
 
-// the values the 8-bit form of a row stands for
-template <int ACT, bool VEC>
-__device__ __forceinline__ void act8_load16(const NormParams& p, int64_t row, bool ok, int g, int G, float (&v)[16]) {
-    if constexpr (VEC) {
-        if (ok && g * 16 < p.C) {
-            const uint4 w = *reinterpret_cast<const uint4*>(p.codes + row * p.cs + g * 16);
-            const float s = act8_scale(p.exps[row * p.es + (g >> 1)]);
-            act8_value4<ACT>(w.x, s, v);
-            act8_value4<ACT>(w.y, s, v + 4);
-            act8_value4<ACT>(w.z, s, v + 8);
-            act8_value4<ACT>(w.w, s, v + 12);
+// sixteen channels of the 8-bit form of a row, as loaded
+template <int ACT, int MODE>
+struct NormRow8 {
+    uint32_t w[MODE == kVec ? 4 : 16], e[MODE == kVec ? 1 : 16];
+    __device__ __forceinline__ void load(const NormParams& p, int64_t row, bool ok, int g, int G) {
+        if constexpr (MODE == kVec) {
+            w[0] = w[1] = w[2] = w[3] = e[0] = 0u;
+            if (ok && g * 16 < p.C) {
+                const uint4 c = *reinterpret_cast<const uint4*>(p.codes + row * p.cs + g * 16);
+                w[0] = c.x;
+                w[1] = c.y;
+                w[2] = c.z;
+                w[3] = c.w;
+                e[0] = p.exps[row * p.es + (g >> 1)];
+            }
         } else {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) v[k] = 0.f;
-        }
-    } else {
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            const int c = norm_col<VEC>(g, G, k);
-            v[k] = ok && c < p.C ? act8_value<ACT>(p.codes[row * p.cs + c]) * act8_scale(p.exps[row * p.es + (c >> 5)])
-                                 : 0.f;
+            for (int k = 0; k < 16; ++k) {
+                const int c = norm_col<MODE>(g, k);
+                w[k] = e[k] = 0u;
+                if (ok && c < p.C) {
+                    w[k] = p.codes[row * p.cs + c];
+                    e[k] = p.exps[row * p.es + (c >> 5)];
+                }
+            }
         }
     }
-}
+    __device__ __forceinline__ void values(float2 (&v)[8]) const {
+        if constexpr (MODE == kVec) {
+            const float s = act8_scale(e[0]);
+            float u[16];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) act8_value4<ACT>(w[q], s, u + 4 * q);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = make_float2(u[2 * k], u[2 * k + 1]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                v[k] = make_float2(act8_value<ACT>(w[2 * k]) * act8_scale(e[2 * k]),
+                                   act8_value<ACT>(w[2 * k + 1]) * act8_scale(e[2 * k + 1]));
+        }
+    }
+};
 
 // ---------------------------------------------------------------------------
 // sums over the lanes of a row
@@ -296,16 +369,19 @@ __device__ __forceinline__ void act8_load16(const NormParams& p, int64_t row, bo
 // ---------------------------------------------------------------------------
 constexpr int kNormThreads = 256;   // rows of up to 512 channels: 256 / G of them per block
 constexpr int kNormMaxWarps = 16;   // rows of up to 8192 channels: one block, a warp per 512
+// blocks per SM; the element-wise rows hold sixteen addresses' worth of registers more
+constexpr int kNormFwdBlocks = 4, kNormFwdBlocksBy = 3, kNormBwdBlocks = 2;
 
 // Sums over the G lanes of this lane's row, the same bits in every lane.  Rows
 // of more than one warp meet in shared memory; `turn` alternates between two
 // buffers, so one barrier per sum is enough.
+template <bool WIDE>
 __device__ __forceinline__ float2 row_sum2(float2 v, int G, float2 (*red)[kNormMaxWarps], int& turn) {
     for (int m = 1; m < 32 && m < G; m <<= 1) {
         v.x += __shfl_xor_sync(0xFFFFFFFFu, v.x, m);
         v.y += __shfl_xor_sync(0xFFFFFFFFu, v.y, m);
     }
-    if (G > 32) {
+    if constexpr (WIDE) {
         if ((threadIdx.x & 31) == 0) red[turn][threadIdx.x >> 5] = v;
         __syncthreads();
         v = red[turn][0];
@@ -317,55 +393,100 @@ __device__ __forceinline__ float2 row_sum2(float2 v, int G, float2 (*red)[kNormM
     }
     return v;
 }
+template <bool WIDE>
+__device__ __forceinline__ float row_sum(float v, int G, float2 (*red)[kNormMaxWarps], int& turn) {
+    if constexpr (WIDE) {
+        return row_sum2<true>(make_float2(v, 0.f), G, red, turn).x;
+    } else {
+        for (int m = 1; m < 32 && m < G; m <<= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, m);
+        return v;
+    }
+}
+__device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
 
 // ---------------------------------------------------------------------------
 // forward; with RESTORE the row comes from its 8-bit form and its statistics
 // ---------------------------------------------------------------------------
-template <typename TX, typename TY, int ACT, bool VEC, bool RESTORE>
-__global__ void __launch_bounds__(512) tri_norm_fwd_kernel(const __grid_constant__ NormParams p) {
+template <typename TX, typename TY, int ACT, int MODE, bool RESTORE, bool WIDE>
+__global__ void __launch_bounds__(WIDE ? 32 * kNormMaxWarps : kNormThreads, WIDE ? 1 : MODE == kVec ? kNormFwdBlocks : kNormFwdBlocksBy)
+    tri_norm_fwd_kernel(const __grid_constant__ NormParams p) {
     __shared__ float2 red[2][kNormMaxWarps];
+    __shared__ __align__(16) float sh_w[WIDE ? 4 : 512], sh_b[WIDE ? 4 : 512];
     const bool dead = device_error_pending();
-    const int G = p.lanes;
-    const int g = G > 32 ? static_cast<int>(threadIdx.x) : static_cast<int>(threadIdx.x) & (G - 1);
-    const int per_block = blockDim.x / G, sub = threadIdx.x / G;
+    const int G = MODE == kVec || WIDE ? p.lanes : MODE;
+    const int g = WIDE ? static_cast<int>(threadIdx.x) : static_cast<int>(threadIdx.x) & (G - 1);
+    const int per_block = WIDE ? 1 : kNormThreads / G, sub = WIDE ? 0 : threadIdx.x / G;
     int turn = 0;
-    float w[16], b[16];
-    load_param16<VEC>(p.w, p.w_bf16, 1.f, g, G, p.C, w);
-    load_param16<VEC>(p.b, p.w_bf16, 0.f, g, G, p.C, b);
-    // the loop runs for whole blocks: rows past R are computed on zeros and not stored
-    for (int64_t base = static_cast<int64_t>(blockIdx.x) * per_block; base < p.R;
-         base += static_cast<int64_t>(gridDim.x) * per_block) {
-        const int64_t row = base + sub;
-        const bool ok = row < p.R, st = ok && !dead;
-        float v[16], mean, rstd;
+    NormParam<MODE, WIDE> w, b;
+    w.init(p.w, p.w_bf16, 1.f, g, G, p.C, sh_w);
+    b.init(p.b, p.w_bf16, 0.f, g, G, p.C, sh_b);
+    NormRow<TX, MODE> next;
+    NormRow8<ACT, MODE> next8;
+    float mean = 0.f, rstd = 0.f;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * per_block;
+    int64_t base = static_cast<int64_t>(blockIdx.x) * per_block;
+    // rows are loaded one round ahead, but for 8-bit rows byte by byte, whose 32 loads do not fit
+    constexpr bool kAhead = MODE == kVec || !RESTORE;
+    const auto load = [&](int64_t row) {
         if constexpr (RESTORE) {
-            act8_load16<ACT, VEC>(p, row, ok, g, G, v);
+            const bool ok = row < p.R;
+            next8.load(p, row, ok, g, G);
             mean = ok ? p.stats[row] : 0.f;
             rstd = ok ? p.stats[p.R + row] : 0.f;
-#pragma unroll
-            for (int k = 0; k < 16; ++k) v[k] -= mean;
         } else {
-            load16<TX, VEC>(p.x, row * p.xs, ok, g, G, p.C, v);
-            if constexpr (ACT != ACT_NONE) act8_emit<ACT, VEC>(p, row, st, g, G, v);
-            float s = 0.f;
+            next.load(p.x, row * p.xs, row < p.R, g, G, p.C);
+        }
+    };
+    if constexpr (kAhead) load(base + sub);
+    if constexpr (!WIDE) __syncthreads();
+    // the loop runs for whole blocks: rows past R are computed on zeros and not stored
+    for (; base < p.R; base += step) {
+        const int64_t row = base + sub;
+        const bool st = row < p.R && !dead;
+        float2 v[8];
+        if constexpr (RESTORE) {
+            if constexpr (!kAhead) load(row);
+            next8.values(v);
+            const float m = mean, r = rstd;
+            if constexpr (kAhead) load(row + step);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) s += v[k];
-            mean = row_sum2(make_float2(s, 0.f), G, red, turn).x * p.inv_c;
-            s = 0.f;
+            for (int k = 0; k < 8; ++k) v[k] = fmul2(fadd2(v[k], splat(-m)), splat(r));
+        } else {
+            next.values(v);
+            load(row + step);
+            if constexpr (ACT != ACT_NONE) act8_emit<ACT, MODE>(p, row, st, g, G, v);
+            float2 s = fadd2(v[0], v[1]);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                v[k] = norm_col<VEC>(g, G, k) < p.C ? v[k] - mean : 0.f;
-                s = fmaf(v[k], v[k], s);
+            for (int k = 2; k < 8; ++k) s = fadd2(s, v[k]);
+            mean = row_sum<WIDE>(s.x + s.y, G, red, turn) * p.inv_c;
+            s = splat(0.f);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                v[k] = fadd2(v[k], splat(-mean));
+                if constexpr (MODE != kVec) {
+                    if (norm_col<MODE>(g, 2 * k) >= p.C) v[k].x = 0.f;
+                    if (norm_col<MODE>(g, 2 * k + 1) >= p.C) v[k].y = 0.f;
+                }
+                s = ffma2(v[k], v[k], s);
             }
-            rstd = rsqrtf(fmaf(row_sum2(make_float2(s, 0.f), G, red, turn).x, p.inv_c, p.eps));
+            const float own = MODE != kVec || g * 16 < p.C ? s.x + s.y : 0.f;
+            rstd = rsqrtf(fmaf(row_sum<WIDE>(own, G, red, turn), p.inv_c, p.eps));
             if (st && g == 0) {
                 p.stats[row] = mean;
                 p.stats[p.R + row] = rstd;
             }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = fmul2(v[k], splat(rstd));
         }
 #pragma unroll
-        for (int k = 0; k < 16; ++k) v[k] = fmaf(v[k] * rstd, w[k], b[k]);
-        store16<TY, VEC>(p.y, row * p.ys, st, g, G, p.C, v);
+        for (int q = 0; q < 4; ++q) {
+            float2 wa, wb, ba, bb;
+            w.get4(q, g, G, wa, wb);
+            b.get4(q, g, G, ba, bb);
+            v[2 * q] = ffma2(v[2 * q], wa, ba);
+            v[2 * q + 1] = ffma2(v[2 * q + 1], wb, bb);
+        }
+        store16<TY, MODE>(p.y, row * p.ys, st, g, G, p.C, v);
     }
 }
 
@@ -375,83 +496,116 @@ __global__ void __launch_bounds__(512) tri_norm_fwd_kernel(const __grid_constant
 // The block's share of dw and db leaves as one partial sum; the shares are
 // added in block order by tri_ordered_sum_kernel.  The number of blocks is a
 // function of the sizes alone, and so is every order of additions.
-template <typename TX, typename TY, int ACT, bool VEC>
-__global__ void __launch_bounds__(512) tri_norm_bwd_kernel(const __grid_constant__ NormParams p) {
+template <typename TX, typename TY, int ACT, int MODE, bool WIDE>
+__global__ void __launch_bounds__(WIDE ? 32 * kNormMaxWarps : kNormThreads, WIDE ? 1 : kNormBwdBlocks)
+    tri_norm_bwd_kernel(const __grid_constant__ NormParams p) {
     __shared__ float2 red[2][kNormMaxWarps];
-    __shared__ float sums[kNormThreads / 32][2][512];
+    __shared__ __align__(16) float sums[WIDE ? 1 : kNormThreads / 32][2][WIDE ? 1 : 512];
+    __shared__ __align__(16) float sh_w[WIDE ? 4 : 512];
     const bool dead = device_error_pending();
-    const int G = p.lanes;
-    const int g = G > 32 ? static_cast<int>(threadIdx.x) : static_cast<int>(threadIdx.x) & (G - 1);
-    const int per_block = blockDim.x / G, sub = threadIdx.x / G;
+    const int G = MODE == kVec || WIDE ? p.lanes : MODE;
+    const int g = WIDE ? static_cast<int>(threadIdx.x) : static_cast<int>(threadIdx.x) & (G - 1);
+    const int per_block = WIDE ? 1 : kNormThreads / G, sub = WIDE ? 0 : threadIdx.x / G;
     int turn = 0;
-    float w[16], dw[16], db[16];
-    load_param16<VEC>(p.w, p.w_bf16, 1.f, g, G, p.C, w);
+    NormParam<MODE, WIDE> w;
+    w.init(p.w, p.w_bf16, 1.f, g, G, p.C, sh_w);
+    float2 dw[8], db[8];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) dw[k] = db[k] = 0.f;
-    for (int64_t base = static_cast<int64_t>(blockIdx.x) * per_block; base < p.R;
-         base += static_cast<int64_t>(gridDim.x) * per_block) {
-        const int64_t row = base + sub;
-        const bool ok = row < p.R, st = ok && !dead;
-        float h[16], d[16];
+    for (int k = 0; k < 8; ++k) dw[k] = db[k] = splat(0.f);
+    NormRow<TX, MODE> nx;
+    NormRow8<ACT, MODE> nx8;
+    NormRow<TY, MODE> nd;
+    float mean, rstd;
+    const int64_t step = static_cast<int64_t>(gridDim.x) * per_block;
+    int64_t base = static_cast<int64_t>(blockIdx.x) * per_block;
+    constexpr bool kAhead = MODE == kVec || ACT == ACT_NONE;
+    const auto load = [&](int64_t row) {
+        const bool ok = row < p.R;
         if constexpr (ACT != ACT_NONE)
-            act8_load16<ACT, VEC>(p, row, ok, g, G, h);
+            nx8.load(p, row, ok, g, G);
         else
-            load16<TX, VEC>(p.x, row * p.xs, ok, g, G, p.C, h);
-        load16<TY, VEC>(p.dy, row * p.dys, ok, g, G, p.C, d);
-        const float mean = ok ? p.stats[row] : 0.f, rstd = ok ? p.stats[p.R + row] : 0.f;
-        float2 s = make_float2(0.f, 0.f);
+            nx.load(p.x, row * p.xs, ok, g, G, p.C);
+        nd.load(p.dy, row * p.dys, ok, g, G, p.C);
+        mean = ok ? p.stats[row] : 0.f;
+        rstd = ok ? p.stats[p.R + row] : 0.f;
+    };
+    if constexpr (kAhead) load(base + sub);
+    if constexpr (!WIDE) __syncthreads();
+    for (; base < p.R; base += step) {
+        const int64_t row = base + sub;
+        const bool st = row < p.R && !dead;
+        float2 h[8], d[8];
+        if constexpr (!kAhead) load(row);
+        if constexpr (ACT != ACT_NONE)
+            nx8.values(h);
+        else
+            nx.values(h);
+        nd.values(d);
+        const float m = mean, r = rstd;
+        if constexpr (kAhead) load(row + step);
+        float2 sa = splat(0.f), sb = splat(0.f);
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            h[k] = (h[k] - mean) * rstd;
-            dw[k] = fmaf(d[k], h[k], dw[k]);
-            db[k] += d[k];
-            d[k] *= w[k];
-            s.x += d[k];
-            s.y = fmaf(d[k], h[k], s.y);
+        for (int q = 0; q < 4; ++q) {
+            float2 ww[2];
+            w.get4(q, g, G, ww[0], ww[1]);
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int k = 2 * q + x;
+                h[k] = fmul2(fadd2(h[k], splat(-m)), splat(r));
+                dw[k] = ffma2(d[k], h[k], dw[k]);
+                db[k] = fadd2(db[k], d[k]);
+                d[k] = fmul2(d[k], ww[x]);
+                sa = fadd2(sa, d[k]);
+                sb = ffma2(d[k], h[k], sb);
+            }
         }
         if (p.dx) {
-            s = row_sum2(s, G, red, turn);
-            const float c1 = s.x * p.inv_c, c2 = s.y * p.inv_c;
+            const float2 s = row_sum2<WIDE>(make_float2(sa.x + sa.y, sb.x + sb.y), G, red, turn);
+            const float2 c1 = splat(s.x * p.inv_c), c2 = splat(-s.y * p.inv_c);
+            const float2 n1 = make_float2(-c1.x, -c1.y);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) d[k] = rstd * (d[k] - fmaf(h[k], c2, c1));
-            store16<TX, VEC>(p.dx, row * p.dxs, st, g, G, p.C, d);
+            for (int k = 0; k < 8; ++k) d[k] = fmul2(fadd2(d[k], ffma2(h[k], c2, n1)), splat(r));
+            store16<TX, MODE>(p.dx, row * p.dxs, st, g, G, p.C, d);
         }
     }
     if (!p.partial) return;  // the same for every thread
     float* out = p.partial + static_cast<int64_t>(blockIdx.x) * 2 * p.C;
-    if (G > 32) {
+    if constexpr (WIDE) {
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
-            const int c = norm_col<VEC>(g, G, k);
+            const int c = norm_col<MODE>(g, k);
             if (c < p.C && !dead) {
-                out[c] = dw[k];
-                out[p.C + c] = db[k];
+                out[c] = k & 1 ? dw[k / 2].y : dw[k / 2].x;
+                out[p.C + c] = k & 1 ? db[k / 2].y : db[k / 2].x;
             }
         }
-        return;
-    }
-    // the rows of a warp, then the warps of the block
-    for (int m = G; m < 32; m <<= 1) {
+    } else {
+        // the rows of a warp, then the warps of the block
+        for (int m = G; m < 32; m <<= 1) {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            dw[k] += __shfl_xor_sync(0xFFFFFFFFu, dw[k], m);
-            db[k] += __shfl_xor_sync(0xFFFFFFFFu, db[k], m);
+            for (int k = 0; k < 8; ++k) {
+                dw[k].x += __shfl_xor_sync(0xFFFFFFFFu, dw[k].x, m);
+                dw[k].y += __shfl_xor_sync(0xFFFFFFFFu, dw[k].y, m);
+                db[k].x += __shfl_xor_sync(0xFFFFFFFFu, db[k].x, m);
+                db[k].y += __shfl_xor_sync(0xFFFFFFFFu, db[k].y, m);
+            }
         }
-    }
-    const int warp = threadIdx.x >> 5;
-    if ((threadIdx.x & 31) < G) {
+        const int warp = threadIdx.x >> 5;
+        if ((threadIdx.x & 31) < G) {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-            sums[warp][0][norm_col<VEC>(g, G, k)] = dw[k];
-            sums[warp][1][norm_col<VEC>(g, G, k)] = db[k];
+            for (int k = 0; k < 16; ++k) {
+                sums[warp][0][norm_col<MODE>(g, k)] = k & 1 ? dw[k / 2].y : dw[k / 2].x;
+                sums[warp][1][norm_col<MODE>(g, k)] = k & 1 ? db[k / 2].y : db[k / 2].x;
+            }
         }
-    }
-    __syncthreads();
-    for (int c = threadIdx.x; c < 2 * p.C; c += blockDim.x) {
-        const int which = c >= p.C, col = c - which * p.C;
-        float s = 0.f;
-        for (int q = 0; q < kNormThreads / 32; ++q) s += sums[q][which][col];
-        if (!dead) out[c] = s;
+        __syncthreads();
+        for (int c = threadIdx.x; c < 2 * p.C; c += blockDim.x) {
+            const int which = c >= p.C, col = c - which * p.C;
+            float s = 0.f;
+#pragma unroll
+            for (int q = 0; q < kNormThreads / 32; ++q) s += sums[q][which][col];
+            if (!dead) out[c] = s;
+        }
     }
 }
 
@@ -501,13 +655,17 @@ __global__ void __launch_bounds__(256) tri_act8_kernel(const __grid_constant__ N
         if constexpr (VEC) {
             const bool ok = it < items && blk * 32 + g * 16 < p.C;
             const int unit = blk * 2 + g;
-            float v[16];
+            float2 v[8];
             if constexpr (PACK) {
-                load16<TX, true>(p.x, row * p.xs, ok, unit, 2, p.C, v);
-                act8_emit<ACT, true>(p, row, ok && !dead, unit, 2, v);
+                NormRow<TX, kVec> r;
+                r.load(p.x, row * p.xs, ok, unit, 2, p.C);
+                r.values(v);
+                act8_emit<ACT, kVec>(p, row, ok && !dead, unit, 2, v);
             } else {
-                act8_load16<ACT, true>(p, row, ok, unit, 2, v);
-                store16<TX, true>(p.y, row * p.ys, ok && !dead, unit, 2, p.C, v);
+                NormRow8<ACT, kVec> r;
+                r.load(p, row, ok, unit, 2);
+                r.values(v);
+                store16<TX, kVec>(p.y, row * p.ys, ok && !dead, unit, 2, p.C, v);
             }
         } else {
             const int c = blk * 32 + g;
