@@ -168,9 +168,12 @@ tri_attn_status act8_impl(int64_t R, int C, const void* x, int64_t xs, int x_typ
     tri_attn_status st = check_rows(x, R, C, xs, xe, !pack);
     if (st || (st = check_act8(act, R, C, pack)) || (st = ensure_device())) return st;
     if (R == 0) return TRI_ATTN_OK;
+    const bool vec = C % 16 == 0 && vec_rows(x, xs, xe) && vec_act8(act);
+    const int pieces = (C + 511) / 512;
     NormParams p{};
     p.R = R;
     p.C = C;
+    p.lanes = norm_shape(std::min(C, 512), vec).lanes;
     p.x = x;
     p.xs = xs;
     p.y = const_cast<void*>(x);
@@ -179,21 +182,21 @@ tri_attn_status act8_impl(int64_t R, int C, const void* x, int64_t xs, int x_typ
     p.cs = act.codes_stride;
     p.exps = static_cast<uint8_t*>(act.exps);
     p.es = act.exps_stride;
-    const bool vec = C % 16 == 0 && vec_rows(x, xs, xe) && vec_act8(act);
-    const int64_t per = vec ? 128 : 8, items = R * ((C + 31) / 32);
-    const unsigned grid = static_cast<unsigned>(std::min<int64_t>((items + per - 1) / per, 148 * 16));
+    const int64_t per = tri::kNormThreads / p.lanes, items = R * pieces;
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>((items + per - 1) / per, 148 * (vec ? tri::kAct8Blocks : tri::kAct8BlocksBy) * 2));
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    with_bool(vec, [&](auto v) {
-        with_types(x_type, x_type, [&](auto tx, auto ty) {
-            using TX = decltype(tx);
-            if constexpr (std::is_same<TX, decltype(ty)>::value)
-                with_kind(act.kind, [&](auto k) {
-                    with_bool(pack, [&](auto pk) {
-                        tri::tri_act8_kernel<TX, decltype(k)::value, decltype(v)::value, decltype(pk)::value>
-                            <<<grid, 256, 0, cs>>>(p);
+    with_mode(vec, p.lanes, [&](auto m, auto wd) {
+        if constexpr (!decltype(wd)::value)  // pieces are no wider than a warp
+            with_types(x_type, x_type, [&](auto tx, auto ty) {
+                using TX = decltype(tx);
+                if constexpr (std::is_same<TX, decltype(ty)>::value)
+                    with_kind(act.kind, [&](auto k) {
+                        with_bool(pack, [&](auto pk) {
+                            tri::tri_act8_kernel<TX, decltype(k)::value, decltype(m)::value, decltype(pk)::value>
+                                <<<grid, tri::kNormThreads, 0, cs>>>(p);
+                        });
                     });
-                });
-        });
+            });
     });
     return launched();
 }

@@ -257,9 +257,14 @@ __device__ __forceinline__ void act8_value4(uint32_t w, float scale, float* v) {
     }
 }
 
-// this lane's sixteen channels into the 8-bit form of their row; every lane of the warp calls it
+// this lane's sixteen channels, from channel c0 of their row on, into its 8-bit form; every lane of
+// the warp calls it
 template <int ACT, int MODE>
-__device__ __forceinline__ void act8_emit(const NormParams& p, int64_t row, bool ok, int g, int G, const float2 (&u)[8]) {
+__device__ __forceinline__ void act8_emit(const NormParams& p, int64_t row, bool ok, int g, int G, const float2 (&u)[8],
+                                          int c0 = 0) {
+    const int C = p.C - c0;
+    uint8_t* codes = p.codes + row * p.cs + c0;
+    uint8_t* exps = p.exps + row * p.es + c0 / 32;
     float v[16];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
@@ -280,9 +285,9 @@ __device__ __forceinline__ void act8_emit(const NormParams& p, int64_t row, bool
             w[q] = act8_code2<ACT>(v[4 * q], v[4 * q + 1], inv) | act8_code2<ACT>(v[4 * q + 2], v[4 * q + 3], inv) << 16;
             if (eb == 255u) w[q] = 0u;
         }
-        if (ok && g * 16 < p.C) {
-            *reinterpret_cast<uint4*>(p.codes + row * p.cs + g * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-            if ((g & 1) == 0) p.exps[row * p.es + (g >> 1)] = static_cast<uint8_t>(eb);
+        if (ok && g * 16 < C) {
+            *reinterpret_cast<uint4*>(codes + g * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+            if ((g & 1) == 0) exps[g >> 1] = static_cast<uint8_t>(eb);
         }
     } else {
         uint32_t a[16];
@@ -291,7 +296,7 @@ __device__ __forceinline__ void act8_emit(const NormParams& p, int64_t row, bool
         if constexpr (MODE == kBy32) {
 #pragma unroll
             for (int k = 0; k < 16; ++k)
-                if (32 * k < p.C) a[k] = __reduce_max_sync(0xFFFFFFFFu, a[k]);
+                if (32 * k < C) a[k] = __reduce_max_sync(0xFFFFFFFFu, a[k]);
         } else {  // a block is eight k of four lanes
 #pragma unroll
             for (int s = 0; s < 16; s += 8) {
@@ -306,11 +311,11 @@ __device__ __forceinline__ void act8_emit(const NormParams& p, int64_t row, bool
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
             const int c = norm_col<MODE>(g, k);
-            if (ok && c < p.C) {
+            if (ok && c < C) {
                 const uint32_t eb = act8_exp<ACT>(a[k]);
                 const uint32_t code = eb == 255u ? 0u : act8_code2<ACT>(v[k], 0.f, act8_inv(eb));
-                p.codes[row * p.cs + c] = static_cast<uint8_t>(code);
-                if ((c & 31) == 0) p.exps[row * p.es + (c >> 5)] = static_cast<uint8_t>(eb);
+                codes[c] = static_cast<uint8_t>(code);
+                if ((c & 31) == 0) exps[c >> 5] = static_cast<uint8_t>(eb);
             }
         }
     }
@@ -320,25 +325,28 @@ __device__ __forceinline__ void act8_emit(const NormParams& p, int64_t row, bool
 template <int ACT, int MODE>
 struct NormRow8 {
     uint32_t w[MODE == kVec ? 4 : 16], e[MODE == kVec ? 1 : 16];
-    __device__ __forceinline__ void load(const NormParams& p, int64_t row, bool ok, int g, int G) {
+    __device__ __forceinline__ void load(const NormParams& p, int64_t row, bool ok, int g, int G, int c0 = 0) {
+        const int C = p.C - c0;
+        const uint8_t* codes = p.codes + row * p.cs + c0;
+        const uint8_t* exps = p.exps + row * p.es + c0 / 32;
         if constexpr (MODE == kVec) {
             w[0] = w[1] = w[2] = w[3] = e[0] = 0u;
-            if (ok && g * 16 < p.C) {
-                const uint4 c = *reinterpret_cast<const uint4*>(p.codes + row * p.cs + g * 16);
+            if (ok && g * 16 < C) {
+                const uint4 c = *reinterpret_cast<const uint4*>(codes + g * 16);
                 w[0] = c.x;
                 w[1] = c.y;
                 w[2] = c.z;
                 w[3] = c.w;
-                e[0] = p.exps[row * p.es + (g >> 1)];
+                e[0] = exps[g >> 1];
             }
         } else {
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
                 const int c = norm_col<MODE>(g, k);
                 w[k] = e[k] = 0u;
-                if (ok && c < p.C) {
-                    w[k] = p.codes[row * p.cs + c];
-                    e[k] = p.exps[row * p.es + (c >> 5)];
+                if (ok && c < C) {
+                    w[k] = codes[c];
+                    e[k] = exps[c >> 5];
                 }
             }
         }
@@ -638,51 +646,38 @@ __global__ void __launch_bounds__(1024) tri_ordered_sum_kernel(const float* __re
 // ---------------------------------------------------------------------------
 // an activation into and out of its 8-bit form
 // ---------------------------------------------------------------------------
-// VEC: two lanes per block of 32 channels, sixteen each; else a warp per block.
-template <typename TX, int ACT, bool VEC, bool PACK>
-__global__ void __launch_bounds__(256) tri_act8_kernel(const __grid_constant__ NormParams p) {
+// The lanes share a row as in the norm; rows of more than 512 channels are cut
+// into pieces of 512, a warp each.  What hides the latency here is many warps.
+constexpr int kAct8Blocks = 6, kAct8BlocksBy = 4;  // per SM
+template <typename TX, int ACT, int MODE, bool PACK>
+__global__ void __launch_bounds__(kNormThreads, MODE == kVec ? kAct8Blocks : kAct8BlocksBy)
+    tri_act8_kernel(const __grid_constant__ NormParams p) {
     const bool dead = device_error_pending();
-    constexpr int kLanes = VEC ? 2 : 32;
-    const int nblk = (p.C + 31) / 32;
-    const int64_t items = p.R * nblk;
-    const int g = threadIdx.x % kLanes;
-    constexpr int kPer = 256 / kLanes;
-    for (int64_t base = static_cast<int64_t>(blockIdx.x) * kPer; base < items;
-         base += static_cast<int64_t>(gridDim.x) * kPer) {
-        const int64_t it = base + threadIdx.x / kLanes;
-        const int64_t row = it / nblk;
-        const int blk = static_cast<int>(it - row * nblk);
-        if constexpr (VEC) {
-            const bool ok = it < items && blk * 32 + g * 16 < p.C;
-            const int unit = blk * 2 + g;
-            float2 v[8];
-            if constexpr (PACK) {
-                NormRow<TX, kVec> r;
-                r.load(p.x, row * p.xs, ok, unit, 2, p.C);
-                r.values(v);
-                act8_emit<ACT, kVec>(p, row, ok && !dead, unit, 2, v);
-            } else {
-                NormRow8<ACT, kVec> r;
-                r.load(p, row, ok, unit, 2);
-                r.values(v);
-                store16<TX, kVec>(p.y, row * p.ys, ok && !dead, unit, 2, p.C, v);
-            }
+    const int G = MODE == kVec ? p.lanes : MODE;
+    const int g = static_cast<int>(threadIdx.x) & (G - 1), per_block = kNormThreads / G;
+    const int pieces = (p.C + 511) / 512;
+    const int64_t items = p.R * pieces, step = static_cast<int64_t>(gridDim.x) * per_block;
+    for (int64_t base = static_cast<int64_t>(blockIdx.x) * per_block; base < items; base += step) {
+        const int64_t item = base + threadIdx.x / G;
+        const bool ok = item < items;
+        int64_t row = item;
+        int c0 = 0;
+        if (pieces > 1) {
+            row = item / pieces;
+            c0 = static_cast<int>(item - row * pieces) * 512;
+        }
+        // a piece ends where the next one begins: the lanes cover no more than 512 channels
+        float2 v[8];
+        if constexpr (PACK) {
+            NormRow<TX, MODE> r;
+            r.load(p.x, row * p.xs + c0, ok, g, G, p.C - c0);
+            r.values(v);
+            act8_emit<ACT, MODE>(p, row, ok && !dead, g, G, v, c0);
         } else {
-            const int c = blk * 32 + g;
-            const bool ok = it < items && c < p.C;
-            if constexpr (PACK) {
-                const float v = ok ? to_f32(static_cast<const TX*>(p.x)[row * p.xs + c]) : 0.f;
-                const uint32_t a = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(v) & 0x7FFFFFFFu);
-                const uint32_t eb = act8_exp<ACT>(a);
-                if (ok && !dead) {
-                    p.codes[row * p.cs + c] =
-                        static_cast<uint8_t>(eb == 255u ? 0u : act8_code2<ACT>(v, 0.f, act8_inv(eb)));
-                    if (g == 0) p.exps[row * p.es + blk] = static_cast<uint8_t>(eb);
-                }
-            } else if (ok && !dead) {
-                static_cast<TX*>(p.y)[row * p.ys + c] = from_f32<TX>(
-                    act8_value<ACT>(p.codes[row * p.cs + c]) * act8_scale(p.exps[row * p.es + blk]));
-            }
+            NormRow8<ACT, MODE> r;
+            r.load(p, row, ok, g, G, c0);
+            r.values(v);
+            store16<TX, MODE>(p.y, row * p.ys + c0, ok && !dead, g, G, p.C - c0, v);
         }
     }
 }
