@@ -454,12 +454,18 @@ size_t tri_norm_bwd_workspace_bytes(int64_t R, int C);
 
 tri_attn_status tri_norm_bwd(const tri_norm_bwd_args *args, tri_attn_stream_t stream);
 
-/* act = x in 8 bits; x [R,C] of type x_type with the given row stride. */
-tri_attn_status tri_act8_pack(int64_t R, int C, const void *x, int64_t x_stride, int x_type, tri_act8 act,
-                              tri_attn_stream_t stream);
-/* x = the values act stands for, rounded to x_type. */
-tri_attn_status tri_act8_unpack(int64_t R, int C, tri_act8 act, void *x, int64_t x_stride, int x_type,
-                                tri_attn_stream_t stream);
+/* Pack: act = x in 8 bits.  Unpack: x = the values act stands for, rounded to
+ * x_type.  x is [R,C] of type x_type; any C >= 1. */
+typedef struct {
+    int64_t R;
+    void *x;
+    int64_t x_stride;
+    tri_act8 act;
+    int C, x_type;
+} tri_act8_args;
+
+tri_attn_status tri_act8_pack(const tri_act8_args *args, tri_attn_stream_t stream);
+tri_attn_status tri_act8_unpack(const tri_act8_args *args, tri_attn_stream_t stream);
 
 /* Learned relative position bias by buckets.  For batch b, query i, key j:
  *     delta  = pos_k[b,j] - pos_q[b,i]

@@ -36,7 +36,8 @@ def test_struct_layout_matches_the_header():
 #include <stdio.h>
 #include "tri_attn.h"
 int main(void){
-  printf("%zu %zu %zu %zu %zu %zu %zu\n", sizeof(tri_act8), sizeof(tri_norm_fwd_args),
+  printf("%zu %zu %zu %zu %zu %zu %zu %zu %zu\n", sizeof(tri_act8_args), offsetof(tri_act8_args, x_type),
+         sizeof(tri_act8), sizeof(tri_norm_fwd_args),
          offsetof(tri_norm_fwd_args, act), offsetof(tri_norm_fwd_args, C), offsetof(tri_norm_fwd_args, eps),
          sizeof(tri_norm_bwd_args), offsetof(tri_norm_bwd_args, workspace));
   return 0; }
@@ -47,7 +48,7 @@ int main(void){
         subprocess.run(["gcc", "-I", os.path.join(ROOT, "include"), c, "-o", exe], check=True)
         got = list(map(int, subprocess.run([exe], capture_output=True, text=True, check=True).stdout.split()))
     N, W = Bd.NormFwdArgs, Bd.NormBwdArgs
-    assert got == [ctypes.sizeof(Bd.Act8), ctypes.sizeof(N), N.act.offset, N.C.offset, N.eps.offset, ctypes.sizeof(W),
+    assert got == [ctypes.sizeof(Bd.Act8Args), Bd.Act8Args.x_type.offset, ctypes.sizeof(Bd.Act8), ctypes.sizeof(N), N.act.offset, N.C.offset, N.eps.offset, ctypes.sizeof(W),
                    W.workspace.offset]
 
 
@@ -117,16 +118,18 @@ def test_restore_and_act8_refusals(lib):
     assert lib.tri_norm_fwd(None, None) == lib.tri_norm_bwd(None, None) == lib.tri_norm_restore(None, None) == Bd.TRI_ATTN_ERR_NULL
     assert status(lib.tri_norm_restore, fake(), act__kind=0) == Bd.TRI_ATTN_ERR_UNSUPPORTED
     assert status(lib.tri_norm_restore, fake(), act__codes=None) == Bd.TRI_ATTN_ERR_NULL
-    act = Bd.Act8(0x10000, 128, 0x2000000, 4, 1)
-    x = 0x3000000
-    assert lib.tri_act8_pack(-1, 128, x, 128, 0, act, None) == Bd.TRI_ATTN_ERR_SHAPE
-    assert lib.tri_act8_pack(8, 128, None, 128, 0, act, None) == Bd.TRI_ATTN_ERR_NULL
-    assert lib.tri_act8_pack(8, 128, x, 128, 5, act, None) == Bd.TRI_ATTN_ERR_DTYPE
-    assert lib.tri_act8_pack(8, 129, x, 129, 0, act, None) == Bd.TRI_ATTN_ERR_STRIDE  # code rows would overlap
-    assert lib.tri_act8_unpack(8, 128, act, x, 100, 0, None) == Bd.TRI_ATTN_ERR_STRIDE
-    assert lib.tri_act8_unpack(8, 128, act, x + 1, 128, 0, None) == Bd.TRI_ATTN_ERR_ALIGN
-    act.kind = 0
-    assert lib.tri_act8_unpack(8, 128, act, x, 128, 0, None) == Bd.TRI_ATTN_ERR_UNSUPPORTED
+    assert lib.tri_act8_pack(None, None) == lib.tri_act8_unpack(None, None) == Bd.TRI_ATTN_ERR_NULL
+    for fn, what, want in (
+            (lib.tri_act8_pack, {"R": -1}, Bd.TRI_ATTN_ERR_SHAPE), (lib.tri_act8_pack, {"C": 0}, Bd.TRI_ATTN_ERR_SHAPE),
+            (lib.tri_act8_pack, {"x": None}, Bd.TRI_ATTN_ERR_NULL), (lib.tri_act8_pack, {"x_type": 5}, Bd.TRI_ATTN_ERR_DTYPE),
+            (lib.tri_act8_pack, {"act__codes_stride": 127}, Bd.TRI_ATTN_ERR_STRIDE),  # code rows would overlap
+            (lib.tri_act8_pack, {"act__exps": None}, Bd.TRI_ATTN_ERR_NULL),
+            (lib.tri_act8_unpack, {"x_stride": 100}, Bd.TRI_ATTN_ERR_STRIDE),
+            (lib.tri_act8_unpack, {"x": 0x10001}, Bd.TRI_ATTN_ERR_ALIGN),
+            (lib.tri_act8_unpack, {"act__kind": 0}, Bd.TRI_ATTN_ERR_UNSUPPORTED)):
+        a = Bd.Act8Args()
+        a.R, a.C, a.x, a.x_stride, a.act = 8, 128, 0x3000000, 128, Bd.Act8(0x10000, 128, 0x2000000, 4, 1)
+        assert status(fn, a, **what) == want
 
 
 def test_workspace_bytes(lib):

@@ -109,6 +109,11 @@ class NormBwdArgs(ctypes.Structure):
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t)]
 
 
+class Act8Args(ctypes.Structure):
+    _fields_ = [("R", ctypes.c_int64), ("x", ctypes.c_void_p), ("x_stride", ctypes.c_int64), ("act", Act8),
+                ("C", ctypes.c_int), ("x_type", ctypes.c_int)]
+
+
 class RelposFwdArgs(ctypes.Structure):
     _fields_ = [("B", ctypes.c_int), ("H", ctypes.c_int), ("Nq", ctypes.c_int), ("Nk", ctypes.c_int),
                 ("E", ctypes.c_int), ("table_type", ctypes.c_int), ("table", ctypes.c_void_p),
@@ -131,10 +136,12 @@ assert _FWD_PACK.size == ctypes.sizeof(FwdArgs) and FwdArgs.lse.offset == _FWD_P
 # ... and those of the norm and the relative position bias
 _NORM_PACK = struct.Struct("<qQqQQQqQ" + "QqQqi4x" + "4if4x")
 _NORM_TAIL = struct.Struct("<QqQqQQQQ")
+_ACT8_PACK = struct.Struct("<qQq" + "QqQqi4x" + "2i")
 _RELPOS_PACK = struct.Struct("<6i" + "6Q" + "2q" + "Q4q" * 2)
 _RELPOS_TAIL = struct.Struct("<Q4qQQQ")
 assert _NORM_PACK.size == ctypes.sizeof(NormFwdArgs) and NormFwdArgs.C.offset == _NORM_PACK.size - 24
 assert _NORM_PACK.size + _NORM_TAIL.size == ctypes.sizeof(NormBwdArgs)
+assert _ACT8_PACK.size == ctypes.sizeof(Act8Args)
 assert _RELPOS_PACK.size == ctypes.sizeof(RelposFwdArgs) and RelposFwdArgs.base.offset == _RELPOS_PACK.size - 80
 assert _RELPOS_PACK.size + _RELPOS_TAIL.size == ctypes.sizeof(RelposBwdArgs)
 assert _FWD_PACK.size + _BWD_TAIL.size == ctypes.sizeof(BwdArgs) and BwdArgs.dout.offset == _FWD_PACK.size
@@ -195,17 +202,12 @@ def load() -> ctypes.CDLL:
             lib.tri_attn_set_wait_limit_ns.restype = None
             lib.tri_attn_selftest_expire_wait.argtypes = [ctypes.c_void_p]
             lib.tri_attn_selftest_expire_wait.restype = ctypes.c_int
-            for n in ("tri_norm_fwd", "tri_norm_restore", "tri_norm_bwd", "tri_relpos_fwd", "tri_relpos_bwd"):
+            for n in ("tri_norm_fwd", "tri_norm_restore", "tri_norm_bwd", "tri_act8_pack", "tri_act8_unpack",
+                      "tri_relpos_fwd", "tri_relpos_bwd"):
                 f = getattr(lib, n)
                 f.argtypes, f.restype = [ctypes.c_char_p, ctypes.c_void_p], ctypes.c_int
             lib.tri_norm_bwd_workspace_bytes.argtypes = [ctypes.c_int64, ctypes.c_int]
             lib.tri_norm_bwd_workspace_bytes.restype = ctypes.c_size_t
-            for n in ("tri_act8_pack", "tri_act8_unpack"):
-                getattr(lib, n).restype = ctypes.c_int
-            lib.tri_act8_pack.argtypes = [ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.c_int64, ctypes.c_int,
-                                          Act8, ctypes.c_void_p]
-            lib.tri_act8_unpack.argtypes = [ctypes.c_int64, ctypes.c_int, Act8, ctypes.c_void_p, ctypes.c_int64,
-                                            ctypes.c_int, ctypes.c_void_p]
             lib.tri_relpos_bwd_workspace_bytes.argtypes = [ctypes.c_int] * 6
             lib.tri_relpos_bwd_workspace_bytes.restype = ctypes.c_size_t
             lib.tri_attn_abi_version.argtypes = []
@@ -698,15 +700,15 @@ def tri_norm_bwd(x, codes, exps, kind: int, stats, w, dy, dx, dw, db, workspace,
 def tri_act8_pack(x, codes, exps, kind: int, stream=None) -> None:
     """codes [.., C], exps [.., ceil(C/32)] = x [.., C] (BF16 or FP32) in 8 bits."""
     xp, xs, R, C = _rows(x, "x")
-    act, xt, lib = Act8(*_act8(codes, exps, kind, R, C)), _float_type(x, "x"), _lib or load()
-    _call(lambda a, s: lib.tri_act8_pack(R, C, xp, xs, xt, a, s), act, "tri_act8_pack", stream, x, codes, exps)
+    a = _ACT8_PACK.pack(R, xp, xs, *_act8(codes, exps, kind, R, C), C, _float_type(x, "x"))
+    _call((_lib or load()).tri_act8_pack, a, "tri_act8_pack", stream, x, codes, exps)
 
 
 def tri_act8_unpack(codes, exps, kind: int, x, stream=None) -> None:
     """x [.., C] (BF16 or FP32) = the values that codes and exps stand for."""
     xp, xs, R, C = _rows(x, "x")
-    act, xt, lib = Act8(*_act8(codes, exps, kind, R, C)), _float_type(x, "x"), _lib or load()
-    _call(lambda a, s: lib.tri_act8_unpack(R, C, a, xp, xs, xt, s), act, "tri_act8_unpack", stream, x, codes, exps)
+    a = _ACT8_PACK.pack(R, xp, xs, *_act8(codes, exps, kind, R, C), C, _float_type(x, "x"))
+    _call((_lib or load()).tri_act8_unpack, a, "tri_act8_unpack", stream, x, codes, exps)
 
 
 def _int32(t, name, dims) -> int:

@@ -160,8 +160,12 @@ tri_attn_status norm_fwd_impl(const tri_norm_fwd_args* a, bool restore, tri_attn
     return launched();
 }
 
-tri_attn_status act8_impl(int64_t R, int C, const void* x, int64_t xs, int x_type, const tri_act8& act, bool pack,
-                          tri_attn_stream_t stream) {
+tri_attn_status act8_impl(const tri_act8_args* a, bool pack, tri_attn_stream_t stream) {
+    if (!a) return TRI_ATTN_ERR_NULL;
+    const int64_t R = a->R, xs = a->x_stride;
+    const int C = a->C, x_type = a->x_type;
+    const tri_act8& act = a->act;
+    void* x = a->x;
     if (R < 0 || R > (int64_t{1} << 40) || C < 1) return TRI_ATTN_ERR_SHAPE;
     if (!type_ok(x_type)) return TRI_ATTN_ERR_DTYPE;
     const int64_t xe = type_bytes(x_type);
@@ -176,7 +180,7 @@ tri_attn_status act8_impl(int64_t R, int C, const void* x, int64_t xs, int x_typ
     p.lanes = norm_shape(std::min(C, 512), vec).lanes;
     p.x = x;
     p.xs = xs;
-    p.y = const_cast<void*>(x);
+    p.y = x;
     p.ys = xs;
     p.codes = static_cast<uint8_t*>(act.codes);
     p.cs = act.codes_stride;
@@ -352,14 +356,10 @@ tri_attn_status tri_norm_bwd(const tri_norm_bwd_args* a, tri_attn_stream_t strea
     return launched();
 }
 
-tri_attn_status tri_act8_pack(int64_t R, int C, const void* x, int64_t x_stride, int x_type, tri_act8 act,
-                              tri_attn_stream_t stream) {
-    return act8_impl(R, C, x, x_stride, x_type, act, true, stream);
-}
+tri_attn_status tri_act8_pack(const tri_act8_args* a, tri_attn_stream_t stream) { return act8_impl(a, true, stream); }
 
-tri_attn_status tri_act8_unpack(int64_t R, int C, tri_act8 act, void* x, int64_t x_stride, int x_type,
-                                tri_attn_stream_t stream) {
-    return act8_impl(R, C, x, x_stride, x_type, act, false, stream);
+tri_attn_status tri_act8_unpack(const tri_act8_args* a, tri_attn_stream_t stream) {
+    return act8_impl(a, false, stream);
 }
 
 tri_attn_status tri_relpos_fwd(const tri_relpos_fwd_args* a, tri_attn_stream_t stream) {
@@ -383,10 +383,12 @@ tri_attn_status tri_relpos_fwd(const tri_relpos_fwd_args* a, tri_attn_stream_t s
         p.bs[x] = a->base.stride[x];
         p.os[x] = a->bias.stride[x];
     }
-    const int64_t items = static_cast<int64_t>(a->B) * a->Nq * p.chunks;
-    const dim3 grid(static_cast<unsigned>(std::min<int64_t>((items + tri::kRelThreads - 1) / tri::kRelThreads, 148 * 8)),
-                    (a->H + p.heads - 1) / p.heads);
-    const size_t smem = tri::relpos_fwd_smem(p.nb, p.heads);
+    // all blocks run at once, and hold at least one row of chunks
+    const int64_t items = static_cast<int64_t>(a->B) * a->Nq * p.chunks, threads = tri::kRelThreads;
+    const unsigned head_blocks = (a->H + p.heads - 1) / p.heads;
+    const int64_t at_once = std::max<int64_t>(148 * tri::kRelFwdBlocks / head_blocks, (p.chunks + threads - 1) / threads);
+    const dim3 grid(static_cast<unsigned>(std::min((items + threads - 1) / threads, at_once)), head_blocks);
+    const size_t smem = tri::relpos_fwd_smem(p.nb, p.heads, p.base != nullptr);
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     with_bool(p.base != nullptr, [&](auto v) {
         tri::tri_relpos_fwd_kernel<decltype(v)::value><<<grid, tri::kRelThreads, smem, cs>>>(p);

@@ -75,7 +75,16 @@ struct RelposBuckets {
             dmin = INT32_MIN;
             dmax = INT32_MAX;
         }
-        for (int x = threadIdx.x; x < size; x += blockDim.x) sh_lut[x] = static_cast<uint16_t>(search(lo + x));
+        // each thread fills a run of neighbouring distances: one search, then steps from edge to edge
+        const int run = (size + blockDim.x - 1) / blockDim.x, x0 = threadIdx.x * run;
+        if (x0 < size) {
+            int n = search(lo + x0);
+            int up = n < E ? edges[n] : INT32_MAX;
+            for (int x = x0; x < min(x0 + run, size); ++x) {
+                while (n < E && up <= lo + x) up = ++n < E ? edges[n] : INT32_MAX;
+                sh_lut[x] = static_cast<uint16_t>(n);
+            }
+        }
         __syncthreads();
     }
     // pk - pq, saturating: a difference past 32 bits lies beyond every edge
@@ -110,106 +119,172 @@ struct RelposBuckets {
     }
 };
 
-constexpr int kRelThreads = 256;
-constexpr int kRelHeads = 16;  // heads of the table a forward block holds
-
-// words per table row: heads rounded up to 4, plus 4 so that neighbouring rows start in other banks
-__host__ __device__ constexpr int relpos_pitch(int heads) { return (heads + 3) / 4 * 4 + 4; }
-__host__ constexpr size_t relpos_fwd_smem(int nb, int heads) {
-    return static_cast<size_t>(nb) * relpos_pitch(heads) * 4 + 512 * 4 + kRelLut * 2;
+// eight keys of a row, of which n exist (n < 8 only at the end of a row)
+__device__ __forceinline__ uint4 relpos_load8(const __nv_bfloat16* s, int n) {
+    if (n == 8) return *reinterpret_cast<const uint4*>(s);
+    uint32_t v[8];
+#pragma unroll
+    for (int x = 0; x < 8; ++x) v[x] = x < n ? __bfloat16_as_ushort(s[x]) : 0u;
+    return make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+}
+__device__ __forceinline__ void relpos_values(const uint4& w, float (&v)[8]) {
+    v[0] = bf16lo(w.x); v[1] = bf16hi(w.x);
+    v[2] = bf16lo(w.y); v[3] = bf16hi(w.y);
+    v[4] = bf16lo(w.z); v[5] = bf16hi(w.z);
+    v[6] = bf16lo(w.w); v[7] = bf16hi(w.w);
+}
+__device__ __forceinline__ void relpos_store8(__nv_bfloat16* s, int n, const uint4& w) {
+    if (n == 8) {
+        *reinterpret_cast<uint4*>(s) = w;
+        return;
+    }
+    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int x = 0; x < 8; ++x)
+        if (x < n) s[x] = __ushort_as_bfloat16(static_cast<unsigned short>(v[x / 2] >> (x & 1 ? 16 : 0)));
 }
 
+constexpr int kRelThreads = 256, kRelFwdBlocks = 4;  // per SM
+constexpr int kRelHeads = 16;  // heads of the table a forward block holds
+
+// The table in shared memory, read 8 bytes at a time: BF16 of four heads, or, where
+// a base is added before the rounding, FP32 of two.  A row is an odd number of
+// these, so that sixteen neighbouring rows start in sixteen different pairs of banks.
+__host__ __device__ constexpr int relpos_pitch(int heads, bool base) {
+    return (base ? (heads + 1) / 2 : (heads + 3) / 4) | 1;
+}
+__host__ constexpr size_t relpos_fwd_smem(int nb, int heads, bool base) {
+    return static_cast<size_t>(nb) * relpos_pitch(heads, base) * 8 + 512 * 4 + kRelLut * 2;
+}
+
+// Forward.  A thread keeps to one chunk of eight keys and walks down the rows, as
+// many rows at a step as all threads together hold; neighbouring threads take
+// neighbouring chunks, so a warp's 16-byte stores lie side by side.
 template <bool BASE>
-__global__ void __launch_bounds__(kRelThreads) tri_relpos_fwd_kernel(const __grid_constant__ RelposParams p) {
+__global__ void __launch_bounds__(kRelThreads, kRelFwdBlocks)
+    tri_relpos_fwd_kernel(const __grid_constant__ RelposParams p) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const bool dead = device_error_pending();
     const int h0 = blockIdx.y * p.heads, nh = min(p.heads, p.H - h0);
-    const int pitch = relpos_pitch(p.heads);
-    float* tab = reinterpret_cast<float*>(smem);
-    int32_t* sh_edges = reinterpret_cast<int32_t*>(smem + static_cast<size_t>(p.nb) * pitch * 4);
+    const int pitch = relpos_pitch(p.heads, BASE);
+    uint2* tab = reinterpret_cast<uint2*>(smem);
+    int32_t* sh_edges = reinterpret_cast<int32_t*>(tab + static_cast<size_t>(p.nb) * pitch);
     uint16_t* sh_lut = reinterpret_cast<uint16_t*>(sh_edges + 512);
-    for (int x = threadIdx.x; x < p.nb * pitch; x += kRelThreads) {
-        const int r = x / pitch, h = x - r * pitch;
-        float v = 0.f;
-        if (h < nh) {
-            const int64_t at = static_cast<int64_t>(r) * p.H + h0 + h;
-            v = p.table_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.table)[at])
-                             : static_cast<const float*>(p.table)[at];
+    {
+        constexpr int kPer = BASE ? 2 : 4;  // heads per entry
+        const int per_row = pitch * kPer;
+        for (int x = threadIdx.x; x < p.nb * per_row; x += kRelThreads) {
+            const int r = x / per_row, h = x - r * per_row;
+            float v = 0.f;
+            if (h < nh) {
+                const int64_t at = static_cast<int64_t>(r) * p.H + h0 + h;
+                v = p.table_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p.table)[at])
+                                 : static_cast<const float*>(p.table)[at];
+            }
+            if constexpr (BASE)
+                reinterpret_cast<float*>(tab)[x] = v;
+            else
+                reinterpret_cast<__nv_bfloat16*>(tab)[x] = __float2bfloat16_rn(v);
         }
-        tab[x] = v;
     }
     RelposBuckets bucket;
     bucket.init(sh_edges, sh_lut, p);  // ends with a barrier: the table is in place too
 
-    const int items = p.B * p.Nq * p.chunks;  // < 2^31, checked on the host
-    for (int64_t it64 = static_cast<int64_t>(blockIdx.x) * kRelThreads + threadIdx.x; it64 < items;
-         it64 += static_cast<int64_t>(gridDim.x) * kRelThreads) {
-        const int it = static_cast<int>(it64);
-        const int bi = it / p.chunks, c = it - bi * p.chunks;
-        const int b = bi / p.Nq, i = bi - b * p.Nq;
-        const int j0 = c * 8, nj = min(8, p.Nk - j0);
+    // the grid holds at least one row of chunks (see the launch)
+    const int64_t id = static_cast<int64_t>(blockIdx.x) * kRelThreads + threadIdx.x;
+    const int rstep = static_cast<int>(static_cast<int64_t>(gridDim.x) * kRelThreads / p.chunks);
+    const int row0 = static_cast<int>(id / p.chunks);
+    if (row0 >= rstep) return;  // no barrier follows
+    const int j0 = static_cast<int>(id - static_cast<int64_t>(row0) * p.chunks) * 8, nj = min(8, p.Nk - j0);
+    int key[8], pmin = 0, pmax = 0, g0 = 0;
+    bool one_group = true;
+    const int32_t* gk = nullptr;
+    int last_b = -1;
+    for (int64_t row = row0; row < static_cast<int64_t>(p.B) * p.Nq; row += rstep) {
+        const int b = static_cast<int>(row) / p.Nq, i = static_cast<int>(row) - b * p.Nq;
+        if (b != last_b) {
+            last_b = b;
+            const int32_t* pk = p.pos_k + b * p.ks + j0;
+            gk = p.grp_k ? p.grp_k + b * p.ks + j0 : nullptr;
+            g0 = gk ? gk[0] : 0;
+            one_group = true;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                key[x] = pk[min(x, nj - 1)];
+                pmin = x ? min(pmin, key[x]) : key[x];
+                pmax = x ? max(pmax, key[x]) : key[x];
+                if (gk) one_group &= gk[min(x, nj - 1)] == g0;
+            }
+        }
         const int pq = p.pos_q[b * p.qs + i];
         const int gq = p.grp_q ? p.grp_q[b * p.qs + i] : 0;
-        const int32_t* pk = p.pos_k + b * p.ks + j0;
-        const int32_t* gk = p.grp_k ? p.grp_k + b * p.ks + j0 : nullptr;
         // a chunk whose nearest and farthest key lie in one bucket needs no other look
-        int key[8], at[8];
-        int pmin = INT32_MAX, pmax = INT32_MIN;
-        bool same = true, apart = true;  // all keys of the query's group; none
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-            const int xx = min(x, nj - 1);
-            key[x] = pk[xx];
-            pmin = min(pmin, key[x]);
-            pmax = max(pmax, key[x]);
-            at[x] = gk && gk[xx] != gq;
-            same &= !at[x];
-            apart &= at[x] != 0;
+        int at[8];
+        bool one = false;
+        if (one_group) {
+            at[0] = g0 == gq ? bucket.of(RelposBuckets::distance(pmin, pq)) : p.E + 1;
+            one = g0 != gq || at[0] == bucket.of(RelposBuckets::distance(pmax, pq));
         }
-        const int first = apart ? p.E + 1 : bucket.of(RelposBuckets::distance(pmin, pq));
-        const bool one = apart || (same && first == bucket.of(RelposBuckets::distance(pmax, pq)));
-        if (one) {
+        if (!one) {
 #pragma unroll
-            for (int x = 0; x < 8; ++x) at[x] = first * pitch;
+            for (int x = 0; x < 8; ++x) at[x] = RelposBuckets::distance(key[x], pq);
+            bucket.of8(at);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                if (!one_group && gk[min(x, nj - 1)] != gq) at[x] = p.E + 1;
+                at[x] *= pitch;
+            }
         } else {
-#pragma unroll
-            for (int x = 0; x < 8; ++x) key[x] = RelposBuckets::distance(key[x], pq);
-            bucket.of8(key);
-#pragma unroll
-            for (int x = 0; x < 8; ++x) at[x] = (at[x] ? p.E + 1 : key[x]) * pitch;
+            at[0] *= pitch;
         }
         __nv_bfloat16* out = p.bias + b * p.os[0] + h0 * p.os[1] + i * p.os[2] + j0;
-        const __nv_bfloat16* in = BASE ? p.base + b * p.bs[0] + h0 * p.bs[1] + i * p.bs[2] + j0 : nullptr;
-        for (int h = 0; h < nh; h += 4) {
-            float4 t[8];
+        if constexpr (BASE) {
+            const __nv_bfloat16* in = p.base + b * p.bs[0] + h0 * p.bs[1] + i * p.bs[2] + j0;
+            for (int h = 0; h < nh; h += 2) {
+                const bool two = h + 1 < nh;
+                float u0[8], u1[8];
+                relpos_values(relpos_load8(in, nj), u0);
+                in += p.bs[1];
+                relpos_values(two ? relpos_load8(in, nj) : make_uint4(0u, 0u, 0u, 0u), u1);
+                in += p.bs[1];
+                uint2 e = tab[at[0] + h / 2];
 #pragma unroll
-            for (int x = 0; x < 8; ++x) t[x] = *reinterpret_cast<const float4*>(tab + at[x] + h);
+                for (int x = 0; x < 8; ++x) {
+                    if (x > 0 && !one) e = tab[at[x] + h / 2];
+                    u0[x] += __uint_as_float(e.x);
+                    u1[x] += __uint_as_float(e.y);
+                }
+                if (!dead) {
+                    relpos_store8(out, nj, make_uint4(pack_bf16(u0[0], u0[1]), pack_bf16(u0[2], u0[3]),
+                                                      pack_bf16(u0[4], u0[5]), pack_bf16(u0[6], u0[7])));
+                    if (two)
+                        relpos_store8(out + p.os[1], nj, make_uint4(pack_bf16(u1[0], u1[1]), pack_bf16(u1[2], u1[3]),
+                                                                    pack_bf16(u1[4], u1[5]), pack_bf16(u1[6], u1[7])));
+                }
+                out += 2 * p.os[1];
+            }
+        } else if (one) {
+            for (int h = 0; h < nh; h += 4) {
+                const uint2 e = tab[at[0] + h / 4];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                if (h + q >= nh) break;
-                float v[8];
+                for (int q = 0; q < 4; ++q, out += p.os[1]) {
+                    const uint32_t w = __byte_perm(q < 2 ? e.x : e.y, 0u, q & 1 ? 0x3232 : 0x1010);
+                    if (h + q < nh && !dead) relpos_store8(out, nj, make_uint4(w, w, w, w));
+                }
+            }
+        } else {
+            for (int h = 0; h < nh; h += 4) {
+                uint2 e[8];
 #pragma unroll
-                for (int x = 0; x < 8; ++x) v[x] = q == 0 ? t[x].x : q == 1 ? t[x].y : q == 2 ? t[x].z : t[x].w;
-                __nv_bfloat16* o = out + (h + q) * p.os[1];
-                const __nv_bfloat16* ib = BASE ? in + (h + q) * p.bs[1] : nullptr;
-                if (nj == 8) {
-                    if constexpr (BASE) {
-                        const uint4 w = *reinterpret_cast<const uint4*>(ib);
-                        v[0] += bf16lo(w.x); v[1] += bf16hi(w.x);
-                        v[2] += bf16lo(w.y); v[3] += bf16hi(w.y);
-                        v[4] += bf16lo(w.z); v[5] += bf16hi(w.z);
-                        v[6] += bf16lo(w.w); v[7] += bf16hi(w.w);
-                    }
-                    if (!dead)
-                        *reinterpret_cast<uint4*>(o) = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]),
-                                                                  pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-                } else {
+                for (int x = 0; x < 8; ++x) e[x] = tab[at[x] + h / 4];
 #pragma unroll
-                    for (int x = 0; x < 8; ++x)
-                        if (x < nj && !dead) {
-                            if constexpr (BASE) v[x] += __bfloat162float(ib[x]);
-                            o[x] = __float2bfloat16_rn(v[x]);
-                        }
+                for (int q = 0; q < 4; ++q, out += p.os[1]) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+                        w[x] = __byte_perm(q < 2 ? e[2 * x].x : e[2 * x].y, q < 2 ? e[2 * x + 1].x : e[2 * x + 1].y,
+                                           q & 1 ? 0x7632 : 0x5410);
+                    if (h + q < nh && !dead) relpos_store8(out, nj, make_uint4(w[0], w[1], w[2], w[3]));
                 }
             }
         }
@@ -286,20 +361,6 @@ struct RelposPair {
     }
 };
 
-// eight keys of a row, of which n exist (n < 8 only at the end of a row)
-__device__ __forceinline__ uint4 relpos_load8(const __nv_bfloat16* s, int n) {
-    if (n == 8) return *reinterpret_cast<const uint4*>(s);
-    uint32_t v[8];
-#pragma unroll
-    for (int x = 0; x < 8; ++x) v[x] = x < n ? __bfloat16_as_ushort(s[x]) : 0u;
-    return make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
-}
-__device__ __forceinline__ void relpos_values(const uint4& w, float (&v)[8]) {
-    v[0] = bf16lo(w.x); v[1] = bf16hi(w.x);
-    v[2] = bf16lo(w.y); v[3] = bf16hi(w.y);
-    v[4] = bf16lo(w.z); v[5] = bf16hi(w.z);
-    v[6] = bf16lo(w.w); v[7] = bf16hi(w.w);
-}
 __device__ __forceinline__ float relpos_sum8(const float (&v)[8]) {
     const float2 a = fadd2(make_float2(v[0], v[1]), make_float2(v[2], v[3]));
     const float2 b = fadd2(make_float2(v[4], v[5]), make_float2(v[6], v[7]));

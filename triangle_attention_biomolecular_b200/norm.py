@@ -103,15 +103,15 @@ def norm_forward(x, weight=None, bias=None, eps: float = 1e-5, out_dtype: Option
     """Returns (y, stats, kept): y of x's shape in ``out_dtype`` (default: x's dtype), stats FP32
     [2, rows] (means, reciprocal standard deviations), and kept, x as an :class:`Act8` written
     in the same pass (None without ``checkpoint``)."""
-    if not x.dim() or not x.shape[-1]:
-        raise B.TriAttnError(B.TRI_ATTN_ERR_SHAPE, f"x must have rows of at least one channel, got {list(x.shape)}")
+    x2 = x if x.is_contiguous() else _rows(x)
+    _, _, R, _ = B._rows(x2, "x")
     y = _empty(x, out_dtype)
-    stats = x.new_empty((2, x.numel() // x.shape[-1]), dtype=torch.float32)
+    stats = x.new_empty((2, R), dtype=torch.float32)
     if checkpoint is None:
-        B.tri_norm_fwd(_rows(x), _param(weight), _param(bias), y, stats, eps=eps)
+        B.tri_norm_fwd(x2, _param(weight), _param(bias), y, stats, eps=eps)
         return y, stats, None
     a = _empty8(x, checkpoint)
-    B.tri_norm_fwd(_rows(x), _param(weight), _param(bias), y, stats, a.codes, a.exps, a.kind, eps)
+    B.tri_norm_fwd(x2, _param(weight), _param(bias), y, stats, a.codes, a.exps, a.kind, eps)
     return y, stats, a
 
 
