@@ -483,7 +483,9 @@ tri_attn_status tri_act8_unpack(const tri_act8_args *args, tri_attn_stream_t str
  *             rounded once from the FP32 sum.  Strides as for the attention's
  *             bias: innermost 1, the others non-negative multiples of 8
  *             elements, pointers 16-byte aligned; the bias's own rows must not
- *             overlap.  Elements of a padded row past Nk are left as they were.
+ *             overlap.  Elements of a padded row past Nk are left as they were;
+ *             those of base in the same 16 bytes as the row's last key are read
+ *             (and not used), so they must exist.
  * Sizes: 1 <= B, H, Nq, Nk, with B * Nq * ceil(Nk/8) < 2^31 and H <= 4096. */
 typedef struct {
     int B, H, Nq, Nk, E, table_type;
@@ -502,7 +504,7 @@ tri_attn_status tri_relpos_fwd(const tri_relpos_fwd_args *args, tri_attn_stream_
  * dbias[b,h,i,j], FP32, contiguous, shaped as the table.
  *   f     : the forward's sizes, edges, positions and groups (table, base and
  *           bias are not used)
- *   dbias : BF16 [B,H,Nq,Nk], strides as for base
+ *   dbias : BF16 [B,H,Nq,Nk], strides and the end of a row as for base
  *   workspace : caller-owned device scratch of at least
  *           tri_relpos_bwd_workspace_bytes(...) bytes, 16-byte aligned */
 typedef struct {

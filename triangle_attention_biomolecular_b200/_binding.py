@@ -608,12 +608,15 @@ def _dense(t, name, dtype, shape) -> int:
 
 def _affine(w, b, C):
     """(w pointer, b pointer, type) of the norm's optional weight and bias."""
-    if w is None and b is None:
-        return 0, 0, TRI_TYPE_F32
-    if w is not None and b is not None and w.dtype is not b.dtype:
+    if w is None:
+        if b is None:
+            return 0, 0, TRI_TYPE_F32
+        return 0, _dense(b, "bias", b.dtype, (C,)), _float_type(b, "bias")
+    if b is None:
+        return _dense(w, "weight", w.dtype, (C,)), 0, _float_type(w, "weight")
+    if w.dtype is not b.dtype:
         raise TriAttnError(TRI_ATTN_ERR_DTYPE, f"weight and bias must have one dtype, got {w.dtype} and {b.dtype}")
-    t = b if w is None else w
-    return _dense(w, "weight", t.dtype, (C,)), _dense(b, "bias", t.dtype, (C,)), _float_type(t, "weight and bias")
+    return _dense(w, "weight", w.dtype, (C,)), _dense(b, "bias", w.dtype, (C,)), _float_type(w, "weight and bias")
 
 
 _ACT8_TYPES = {TRI_ACT8_INT8: torch.int8, TRI_ACT8_E4M3: torch.float8_e4m3fn}
@@ -641,18 +644,24 @@ def _workspace(t):
     return t.data_ptr(), t.numel()
 
 
+def _norm_fwd(x, geometry, w, b, y, yp, ys, sp, act, eps, stream, *others) -> None:
+    """tri_norm_fwd for outputs that are known to fit: geometry is _rows of x."""
+    xp, xs, R, C = geometry
+    wp, bp, wt = _affine(w, b, C)
+    a = _NORM_PACK.pack(R, xp, xs, wp, bp, yp, ys, sp, *act, C, _float_type(x, "x"), wt, _float_type(y, "y"), eps)
+    _call((_lib or load()).tri_norm_fwd, a, "tri_norm_fwd", stream, x, w, b, *others)
+
+
 def tri_norm_fwd(x, w, b, y, stats, codes=None, exps=None, kind: int = 0, eps: float = 1e-5, stream=None) -> None:
     """y = (x - mean) * rstd * w + b over the channels of each row; x, y BF16 or FP32, contiguous
     [..., C] or [R, C] with padded rows, w, b [C] or None, stats FP32 [2, R] written (means,
     rstds).  With kind set, codes [.., C] and exps [.., ceil(C/32)] get x in 8 bits in the same
     pass."""
-    xp, xs, R, C = _rows(x, "x")
+    geometry = _rows(x, "x")
+    _, _, R, C = geometry
     yp, ys, _, _ = _rows(y, "y", (R, C))
-    sp = _dense(stats, "stats", torch.float32, (2, R))
-    wp, bp, wt = _affine(w, b, C)
-    act = _act8(codes, exps, kind, R, C) if kind else _NO_ACT8
-    a = _NORM_PACK.pack(R, xp, xs, wp, bp, yp, ys, sp, *act, C, _float_type(x, "x"), wt, _float_type(y, "y"), eps)
-    _call((_lib or load()).tri_norm_fwd, a, "tri_norm_fwd", stream, x, w, b, y, stats, codes, exps)
+    _norm_fwd(x, geometry, w, b, y, yp, ys, _dense(stats, "stats", torch.float32, (2, R)),
+              _act8(codes, exps, kind, R, C) if kind else _NO_ACT8, eps, stream, y, stats, codes, exps)
 
 
 def tri_norm_restore(codes, exps, kind: int, stats, w, b, y, stream=None) -> None:
@@ -668,33 +677,44 @@ def tri_norm_bwd_workspace_bytes(R: int, C: int) -> int:
     return (_lib or load()).tri_norm_bwd_workspace_bytes(R, C)
 
 
+def _norm_bwd(x, codes, exps, kind, stats, w, dy, geometry, x_dtype, into, stream, *others) -> None:
+    """tri_norm_bwd for outputs that are known to fit: geometry is _rows of dy; into: dx's
+    pointer and row stride, dw's and db's pointers, the workspace's pointer and bytes."""
+    dyp, dys, R, C = geometry
+    if x is not None:
+        xp, xs, _, _ = _rows(x, "x", (R, C))
+        act = _NO_ACT8
+    else:
+        xp, xs, act = 0, 0, _act8(codes, exps, kind, R, C)
+    xt = _FLOAT_TYPES.get(x_dtype)
+    if xt is None:
+        raise TriAttnError(TRI_ATTN_ERR_DTYPE, f"x must be bfloat16 or float32, got {x_dtype}")
+    wp, _, wt = _affine(w, None, C)
+    a = _NORM_PACK.pack(R, xp, xs, wp, 0, 0, 0, _dense(stats, "stats", torch.float32, (2, R)), *act, C, xt, wt,
+                        _float_type(dy, "dy"), 0.0) + _NORM_TAIL.pack(dyp, dys, *into)
+    _call((_lib or load()).tri_norm_bwd, a, "tri_norm_bwd", stream, dy, x, codes, exps, stats, w, *others)
+
+
 def tri_norm_bwd(x, codes, exps, kind: int, stats, w, dy, dx, dw, db, workspace, stream=None) -> None:
     """Gradients of the norm for the upstream dy.  x is the forward's input, or None with kind,
     codes and exps set: its 8-bit form.  dx has x's dtype (or is None); dw, db FP32 [C] (or both
     None); workspace a uint8 CUDA tensor of at least tri_norm_bwd_workspace_bytes(R, C) bytes
     (None without dw and db)."""
-    dyp, dys, R, C = _rows(dy, "dy")
-    sp = _dense(stats, "stats", torch.float32, (2, R))
+    geometry = _rows(dy, "dy")
+    _, _, R, C = geometry
     if (x is None) == (not kind):
         raise TriAttnError(TRI_ATTN_ERR_NULL, "tri_norm_bwd: either x or its 8-bit form must be given")
-    if x is not None:
-        xp, xs, _, _ = _rows(x, "x", (R, C))
-        act, xt = _NO_ACT8, _float_type(x, "x")
-    else:
-        xp, xs, act, xt = 0, 0, _act8(codes, exps, kind, R, C), TRI_TYPE_BF16
     dxp, dxs = 0, 0
+    x_dtype = torch.bfloat16 if x is None else x.dtype
     if dx is not None:
         dxp, dxs, _, _ = _rows(dx, "dx", (R, C))
         if x is not None and dx.dtype is not x.dtype:
             raise TriAttnError(TRI_ATTN_ERR_DTYPE, f"dx must be {x.dtype}, got {dx.dtype}")
-        xt = _float_type(dx, "dx")
+        x_dtype = dx.dtype
     if (dw is None) != (db is None):
         raise TriAttnError(TRI_ATTN_ERR_NULL, "tri_norm_bwd: dw and db are given together or not at all")
-    wp, _, wt = _affine(w, None, C)
-    a = _NORM_PACK.pack(R, xp, xs, wp, 0, 0, 0, sp, *act, C, xt, wt, _float_type(dy, "dy"), 0.0) + \
-        _NORM_TAIL.pack(dyp, dys, dxp, dxs, _dense(dw, "dw", torch.float32, (C,)), _dense(db, "db", torch.float32, (C,)),
-                        *_workspace(workspace))
-    _call((_lib or load()).tri_norm_bwd, a, "tri_norm_bwd", stream, dy, x, codes, exps, stats, w, dx, dw, db, workspace)
+    into = (dxp, dxs, _dense(dw, "dw", torch.float32, (C,)), _dense(db, "db", torch.float32, (C,)), *_workspace(workspace))
+    _norm_bwd(x, codes, exps, kind, stats, w, dy, geometry, x_dtype, into, stream, dx, dw, db, workspace)
 
 
 def tri_act8_pack(x, codes, exps, kind: int, stream=None) -> None:

@@ -246,7 +246,7 @@ void relpos_params(RelposParams& p, const tri_relpos_fwd_args& a) {
 
 // launch shape of the backward: a function of the sizes alone
 struct RelposBwdShape {
-    int heads, head_blocks, warps, row_tasks;
+    int heads, head_blocks, warps, row_tasks, run;
     unsigned grid;
     size_t smem;
 };
@@ -271,9 +271,12 @@ RelposBwdShape relpos_bwd_shape(int B, int H, int Nq, int Nk, int nb) {
     s.warps = tri::kRelBwdWarps;
     while (s.warps > 1 && tri::relpos_bwd_smem(nb, s.warps) > tri::kRelBwdSmem) --s.warps;
     s.smem = tri::relpos_bwd_smem(nb, s.warps);
-    // as many tasks as warps run at once, each with at least one batch of rows
+    // as many tasks as warps run at once, each with at least one batch of rows; those with many
+    // take two in a row, so that the buckets in hand last longer
     const int64_t want = std::max<int64_t>(1, 148 * tri::kRelBwdBlocks * s.warps / (tiles * s.head_blocks));
-    s.row_tasks = static_cast<int>(std::min<int64_t>(want, (Nq + tri::kRelRows - 1) / tri::kRelRows));
+    const int64_t batches = (Nq + tri::kRelRows - 1) / tri::kRelRows;
+    s.row_tasks = static_cast<int>(std::min(want, batches));
+    s.run = static_cast<int>(std::min<int64_t>(2, batches / s.row_tasks));
     const int64_t tasks = tiles * s.row_tasks;
     s.grid = static_cast<unsigned>(std::min<int64_t>((tasks + s.warps - 1) / s.warps, 148 * tri::kRelBwdBlocks));
     return s;
@@ -385,6 +388,9 @@ tri_attn_status tri_relpos_fwd(const tri_relpos_fwd_args* a, tri_attn_stream_t s
     }
     // all blocks run at once, and hold at least one row of chunks
     const int64_t items = static_cast<int64_t>(a->B) * a->Nq * p.chunks, threads = tri::kRelThreads;
+    // few rows: the heads go to blocks of their own, four at least (one row of 4096 keys with 16
+    // heads runs on 8 blocks in place of 2)
+    while (p.heads > 4 && (items + threads - 1) / threads * ((a->H + p.heads - 1) / p.heads) < 74) p.heads /= 2;
     const unsigned head_blocks = (a->H + p.heads - 1) / p.heads;
     const int64_t at_once = std::max<int64_t>(148 * tri::kRelFwdBlocks / head_blocks, (p.chunks + threads - 1) / threads);
     const dim3 grid(static_cast<unsigned>(std::min((items + threads - 1) / threads, at_once)), head_blocks);
@@ -419,6 +425,7 @@ tri_attn_status tri_relpos_bwd(const tri_relpos_bwd_args* a, tri_attn_stream_t s
     const RelposBwdShape s = relpos_bwd_shape(f.B, f.H, f.Nq, f.Nk, p.nb);
     p.heads = s.heads;
     p.row_tasks = s.row_tasks;
+    p.run = s.run;
     p.partial = static_cast<float*>(a->workspace);
     p.dbias = static_cast<const __nv_bfloat16*>(a->dbias.ptr);
     for (int x = 0; x < 3; ++x) p.ds[x] = a->dbias.stride[x];

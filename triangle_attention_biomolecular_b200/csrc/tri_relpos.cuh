@@ -33,7 +33,7 @@ struct RelposParams {
     int64_t os[3];
     const __nv_bfloat16* dbias;
     int64_t ds[3];
-    int row_tasks;                 // backward: warps that share the rows of a column tile, batch by batch
+    int row_tasks, run;            // backward: warps that share the rows of a column tile, in runs of batches
     float* partial;                // backward: [gridDim.x][nb][H]
 };
 
@@ -119,13 +119,15 @@ struct RelposBuckets {
     }
 };
 
-// eight keys of a row, of which n exist (n < 8 only at the end of a row)
+// Eight keys of a row, 16 bytes at once; those past the row's end (the last n of
+// a row may be fewer than eight) are read with them and count as 0.
+__device__ __forceinline__ uint4 relpos_cut8(const uint4& w, int n) {
+    const auto keep = [n](uint32_t v, int x) { return n >= x + 2 ? v : n == x + 1 ? v & 0xFFFFu : 0u; };
+    return make_uint4(keep(w.x, 0), keep(w.y, 2), keep(w.z, 4), keep(w.w, 6));
+}
 __device__ __forceinline__ uint4 relpos_load8(const __nv_bfloat16* s, int n) {
-    if (n == 8) return *reinterpret_cast<const uint4*>(s);
-    uint32_t v[8];
-#pragma unroll
-    for (int x = 0; x < 8; ++x) v[x] = x < n ? __bfloat16_as_ushort(s[x]) : 0u;
-    return make_uint4(v[0] | v[1] << 16, v[2] | v[3] << 16, v[4] | v[5] << 16, v[6] | v[7] << 16);
+    const uint4 w = *reinterpret_cast<const uint4*>(s);
+    return n < 8 ? relpos_cut8(w, n) : w;
 }
 __device__ __forceinline__ void relpos_values(const uint4& w, float (&v)[8]) {
     v[0] = bf16lo(w.x); v[1] = bf16hi(w.x);
@@ -138,10 +140,11 @@ __device__ __forceinline__ void relpos_store8(__nv_bfloat16* s, int n, const uin
         *reinterpret_cast<uint4*>(s) = w;
         return;
     }
-    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int x = 0; x < 8; ++x)
-        if (x < n) s[x] = __ushort_as_bfloat16(static_cast<unsigned short>(v[x / 2] >> (x & 1 ? 16 : 0)));
+    if (n & 4) *reinterpret_cast<uint2*>(s) = make_uint2(w.x, w.y);
+    const uint32_t two = n & 4 ? w.z : w.x;
+    if (n & 2) *reinterpret_cast<uint32_t*>(s + (n & 4)) = two;
+    const uint32_t one = n == 7 ? w.w : n == 5 ? w.z : n == 3 ? w.y : w.x;
+    if (n & 1) s[n - 1] = __ushort_as_bfloat16(static_cast<unsigned short>(one));
 }
 
 constexpr int kRelThreads = 256, kRelFwdBlocks = 4;  // per SM
@@ -373,11 +376,10 @@ struct RelposBatch {
     uint4 w[kRelRows];
     int q[kRelRows], g[kRelRows];
     template <bool GROUPS>
-    __device__ __forceinline__ void load(const __nv_bfloat16* s, int64_t step, int nj, const int32_t* pos,
-                                         const int32_t* grp) {
+    __device__ __forceinline__ void load(const __nv_bfloat16* s, int64_t step, const int32_t* pos, const int32_t* grp) {
 #pragma unroll
         for (int u = 0; u < kRelRows; ++u, s += step) {
-            w[u] = relpos_load8(s, nj);
+            w[u] = *reinterpret_cast<const uint4*>(s);
             q[u] = pos[u];
             g[u] = GROUPS ? grp[u] : 0;
         }
@@ -436,14 +438,16 @@ __global__ void __launch_bounds__(kRelBwdWarps * 32, kRelBwdBlocks) tri_relpos_b
         const int64_t step = p.ds[2];
         // a batch of rows, loaded while the one before it is added up
         RelposBatch next;
-        const int stride = p.row_tasks * kRelRows;
-        int i0 = rt * kRelRows;
-        if (i0 + kRelRows <= p.Nq) next.load<GROUPS>(src + i0 * step, step, nj, pos + i0, grp + i0);
-        for (; i0 < p.Nq; i0 += stride) {
+        // `run` batches in a row, then on past the runs of the other tasks
+        const int jump = ((p.row_tasks - 1) * p.run + 1) * kRelRows;
+        int i0 = rt * p.run * kRelRows, left = p.run;
+        if (i0 + kRelRows <= p.Nq) next.load<GROUPS>(src + i0 * step, step, pos + i0, grp + i0);
+        for (int i2; i0 < p.Nq; i0 = i2) {
+            i2 = i0 + (--left ? kRelRows : jump);
+            if (left == 0) left = p.run;
             if (i0 + kRelRows <= p.Nq) {
-                const RelposBatch now = next;
-                const int i2 = i0 + stride;
-                if (i2 + kRelRows <= p.Nq) next.load<GROUPS>(src + i2 * step, step, nj, pos + i2, grp + i2);
+                RelposBatch now = next;
+                if (i2 + kRelRows <= p.Nq) next.load<GROUPS>(src + i2 * step, step, pos + i2, grp + i2);
                 int lo = now.q[0], hi = now.q[0];
                 bool same = one_group, other = GROUPS && one_group;
 #pragma unroll
@@ -459,6 +463,10 @@ __global__ void __launch_bounds__(kRelBwdWarps * 32, kRelBwdBlocks) tri_relpos_b
                 const bool in = same && !is_low && !is_high && lo > hand.qlo && hi < hand.qhi;
                 const bool below = in && lo >= hand.tmax, above = in && hi < hand.tmin;
                 if (other || is_low || is_high || below || above) {
+                    if (nj < 8) {
+#pragma unroll
+                        for (int u = 0; u < kRelRows; ++u) now.w[u] = relpos_cut8(now.w[u], nj);
+                    }
                     float2 a[kRelRows];
 #pragma unroll
                     for (int u = 0; u < kRelRows; ++u)

@@ -103,15 +103,15 @@ def norm_forward(x, weight=None, bias=None, eps: float = 1e-5, out_dtype: Option
     """Returns (y, stats, kept): y of x's shape in ``out_dtype`` (default: x's dtype), stats FP32
     [2, rows] (means, reciprocal standard deviations), and kept, x as an :class:`Act8` written
     in the same pass (None without ``checkpoint``)."""
-    x2 = x if x.is_contiguous() else _rows(x)
-    _, _, R, _ = B._rows(x2, "x")
+    x2 = _rows(x)
+    geometry = B._rows(x2, "x")
     y = _empty(x, out_dtype)
-    stats = x.new_empty((2, R), dtype=torch.float32)
-    if checkpoint is None:
-        B.tri_norm_fwd(x2, _param(weight), _param(bias), y, stats, eps=eps)
-        return y, stats, None
-    a = _empty8(x, checkpoint)
-    B.tri_norm_fwd(x2, _param(weight), _param(bias), y, stats, a.codes, a.exps, a.kind, eps)
+    stats = x.new_empty((2, geometry[2]), dtype=torch.float32)
+    a = None if checkpoint is None else _empty8(x, checkpoint)
+    # y, stats and the 8-bit form are known to fit: only the caller's tensors are checked
+    B._norm_fwd(x2, geometry, _param(weight), _param(bias), y, y.data_ptr(), geometry[3], stats.data_ptr(),
+                B._NO_ACT8 if a is None else (a.codes.data_ptr(), geometry[3], a.exps.data_ptr(), a.exps.shape[-1], a.kind),
+                eps, None)
     return y, stats, a
 
 
@@ -126,17 +126,25 @@ def norm_backward(x, stats, dy, weight=None, need_dx: bool = True, need_dw: Opti
     """Returns (dx, dweight, dbias) for the upstream gradient dy; ``x`` is the forward's input or
     the :class:`Act8` it kept.  dx has x's dtype; dweight and dbias are FP32 [C] (None unless
     ``need_dw``, by default when there is a weight)."""
-    dx = dw = db = ws = None
+    dy2 = _rows(dy)
+    geometry = B._rows(dy2, "dy")
+    _, _, R, C = geometry
+    dx = dw = db = None
+    into = [0, 0, 0, 0, 0, 0]  # dx and its row stride, dw, db, workspace and its size
     if need_dx:
         dx = _empty(dy, x.dtype)
+        into[0], into[1] = dx.data_ptr(), C
     if weight is not None if need_dw is None else need_dw:
-        C = dy.shape[-1]
-        dw, db = dy.new_empty((2, C), dtype=torch.float32).unbind(0)
-        ws = dy.new_empty(B.tri_norm_bwd_workspace_bytes(dy.numel() // C, C), dtype=torch.uint8)
+        grads = dy.new_empty((2, C), dtype=torch.float32)
+        dw, db = grads.unbind(0)
+        need = B.tri_norm_bwd_workspace_bytes(R, C)
+        ws = dy.new_empty(need, dtype=torch.uint8)
+        into[2] = grads.data_ptr()
+        into[3:] = into[2] + 4 * C, ws.data_ptr(), need
     if isinstance(x, Act8):
-        B.tri_norm_bwd(None, _rows(x.codes), _rows(x.exps), x.kind, stats, _param(weight), _rows(dy), dx, dw, db, ws)
+        B._norm_bwd(None, _rows(x.codes), _rows(x.exps), x.kind, stats, _param(weight), dy2, geometry, x.dtype, into, None)
     else:
-        B.tri_norm_bwd(_rows(x), None, None, 0, stats, _param(weight), _rows(dy), dx, dw, db, ws)
+        B._norm_bwd(_rows(x), None, None, 0, stats, _param(weight), dy2, geometry, x.dtype, into, None)
     return dx, dw, db
 
 

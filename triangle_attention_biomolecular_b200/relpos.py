@@ -52,12 +52,17 @@ def relpos_edges_log(per_side: int, max_distance: int, device="cuda") -> torch.T
 
 def _layout(t: torch.Tensor) -> torch.Tensor:
     """t itself if the C ABI accepts its layout (unit inner stride, the others non-negative
-    multiples of 8, 16-byte aligned data), else a copy with rows padded to a multiple of 8."""
-    if t.is_contiguous() and t.shape[3] % 8 == 0 and t.data_ptr() % 16 == 0:
-        return t
-    ok = (t.shape[3] == 1 or t.stride(3) == 1) and t.data_ptr() % 16 == 0
-    if ok and all(n == 1 or (s >= 0 and s % 8 == 0) for n, s in zip(t.shape[:3], t.stride()[:3])):
-        return t
+    multiples of 8, 16-byte aligned data that reach to the end of the last row's last 16 bytes),
+    else a copy with rows padded to a multiple of 8."""
+    n = t.shape[3]
+    if t.data_ptr() % 16 == 0:
+        if n % 8 == 0 and t.is_contiguous():
+            return t
+        lead = [(m - 1) * s for m, s in zip(t.shape[:3], t.stride()[:3])]
+        if (n == 1 or t.stride(3) == 1) and all(s >= 0 and s % 8 == 0 for s in lead) and (
+                n % 8 == 0 or 2 * (t.storage_offset() + sum(lead) + (n + 7) // 8 * 8) <= t.untyped_storage().nbytes()):
+            if all(m == 1 or s % 8 == 0 for m, s in zip(t.shape[:3], t.stride()[:3])):
+                return t
     return _padded(t.shape, t).copy_(t)
 
 
