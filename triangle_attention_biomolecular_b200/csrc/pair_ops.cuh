@@ -111,6 +111,20 @@ void with_mode(bool vec, int lanes, F&& f) {
         lanes == tri::kBy4 ? f(Int<tri::kBy4>{}, std::false_type{}) : f(Int<tri::kBy32>{}, std::false_type{});
 }
 
+// the ordered sum of partial sums, its launch overlapping the end of the kernel that writes them
+void launch_ordered_sum(const float* part, int64_t nparts, int n, float* out0, int n0, float* out1, cudaStream_t cs) {
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((n + 31) / 32);
+    cfg.blockDim = dim3(1024);
+    cfg.stream = cs;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    cudaLaunchKernelEx(&cfg, tri::tri_ordered_sum_kernel, part, static_cast<int>(nparts), n, out0, n0, out1);
+}
+
 tri_attn_status launched() { return cudaGetLastError() == cudaSuccess ? TRI_ATTN_OK : TRI_ATTN_ERR_CUDA; }
 
 tri_attn_status norm_fwd_impl(const tri_norm_fwd_args* a, bool restore, tri_attn_stream_t stream) {
@@ -354,8 +368,7 @@ tri_attn_status tri_norm_bwd(const tri_norm_bwd_args* a, tri_attn_stream_t strea
         });
     }
     if (a->dw)  // with no rows: zeros
-        tri::tri_ordered_sum_kernel<<<(2 * f.C + 31) / 32, 1024, 0, cs>>>(p.partial, static_cast<int>(blocks), 2 * f.C,
-                                                                         a->dw, f.C, a->db);
+        launch_ordered_sum(p.partial, blocks, 2 * f.C, a->dw, f.C, a->db, cs);
     return launched();
 }
 
@@ -434,8 +447,7 @@ tri_attn_status tri_relpos_bwd(const tri_relpos_bwd_args* a, tri_attn_stream_t s
         tri::tri_relpos_bwd_kernel<decltype(v)::value><<<dim3(s.grid, s.head_blocks), s.warps * 32, s.smem, cs>>>(p);
     });
     const int n = p.nb * f.H;
-    tri::tri_ordered_sum_kernel<<<(n + 31) / 32, 1024, 0, cs>>>(p.partial, static_cast<int>(s.grid), n, a->dtable, n,
-                                                               nullptr);
+    launch_ordered_sum(p.partial, s.grid, n, a->dtable, n, nullptr, cs);
     return launched();
 }
 

@@ -498,6 +498,13 @@ __global__ void __launch_bounds__(WIDE ? 32 * kNormMaxWarps : kNormThreads, WIDE
     }
 }
 
+// A kernel launched with programmatic stream serialisation starts while the one
+// before it still runs: grid_dependents_start there allows it (all its blocks have
+// begun), grid_dependency_wait here returns once that kernel has ended and its
+// writes are visible.
+__device__ __forceinline__ void grid_dependents_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---------------------------------------------------------------------------
 // backward: dx row by row, dw and db summed in registers over the block's rows
 // ---------------------------------------------------------------------------
@@ -510,6 +517,7 @@ __global__ void __launch_bounds__(WIDE ? 32 * kNormMaxWarps : kNormThreads, WIDE
     __shared__ float2 red[2][kNormMaxWarps];
     __shared__ __align__(16) float sums[WIDE ? 1 : kNormThreads / 32][2][WIDE ? 1 : 512];
     __shared__ __align__(16) float sh_w[WIDE ? 4 : 512];
+    grid_dependents_start();
     const bool dead = device_error_pending();
     const int G = MODE == kVec || WIDE ? p.lanes : MODE;
     const int g = WIDE ? static_cast<int>(threadIdx.x) : static_cast<int>(threadIdx.x) & (G - 1);
@@ -624,10 +632,11 @@ __global__ void __launch_bounds__(1024) tri_ordered_sum_kernel(const float* __re
                                                                float* __restrict__ out0, int n0,
                                                                float* __restrict__ out1) {
     __shared__ float runs[32][33];
-    const bool dead = device_error_pending();
     const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
     const int i = blockIdx.x * 32 + lane;
     float s = 0.f;
+    grid_dependency_wait();
+    const bool dead = device_error_pending();
     if (i < n)
         for (int q = run; q < nparts; q += 32) s += part[static_cast<int64_t>(q) * n + i];
     runs[run][lane] = s;

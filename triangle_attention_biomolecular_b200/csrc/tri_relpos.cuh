@@ -10,6 +10,7 @@
 #pragma once
 
 #include "sm100.cuh"
+#include "tri_norm.cuh"
 
 namespace tri {
 
@@ -389,6 +390,7 @@ struct RelposBatch {
 template <bool GROUPS>
 __global__ void __launch_bounds__(kRelBwdWarps * 32, kRelBwdBlocks) tri_relpos_bwd_kernel(const __grid_constant__ RelposParams p) {
     extern __shared__ __align__(1024) uint8_t smem[];
+    grid_dependents_start();
     const bool dead = device_error_pending();
     const int warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     float* sums = reinterpret_cast<float*>(smem);  // [warps][nb][32]
