@@ -67,12 +67,13 @@ typedef struct CUstream_st *tri_attn_stream_t;
 typedef enum {
     TRI_ATTN_OK = 0,
     TRI_ATTN_ERR_NULL = 1,           /* a required pointer is NULL                     */
-    TRI_ATTN_ERR_SHAPE = 2,          /* B, N or H out of range                         */
-    TRI_ATTN_ERR_STRIDE = 3,         /* innermost stride != 1, or a stride not a
-                                        non-negative multiple of 8 elements          */
-    TRI_ATTN_ERR_ALIGN = 4,          /* a data pointer is not 16-byte aligned          */
-    TRI_ATTN_ERR_DTYPE = 5,          /* reserved for bindings: wrong element type      */
-    TRI_ATTN_ERR_UNSUPPORTED = 6,    /* d not in {32, 64}, or N > 4096                 */
+    TRI_ATTN_ERR_SHAPE = 2,          /* a size or scalar out of range                  */
+    TRI_ATTN_ERR_STRIDE = 3,         /* innermost stride != 1, or a stride that the call
+                                        does not take                                */
+    TRI_ATTN_ERR_ALIGN = 4,          /* a data pointer is not aligned as the call asks */
+    TRI_ATTN_ERR_DTYPE = 5,          /* wrong element type                             */
+    TRI_ATTN_ERR_UNSUPPORTED = 6,    /* a size past the call's limit (d not in {32, 64},
+                                        N > 4096, C > 8192, ...) or an unknown option  */
     TRI_ATTN_ERR_WORKSPACE = 7,      /* workspace NULL or smaller than required        */
     TRI_ATTN_ERR_ARCH = 8,           /* current device is not sm_100                   */
     TRI_ATTN_ERR_CUDA = 9,           /* a CUDA runtime/driver call failed              */
@@ -399,6 +400,7 @@ typedef struct {
 /* Layer norm over the channels of each row, forward:
  *     mean = sum_c x / C,  rstd = 1 / sqrt(sum_c (x - mean)^2 / C + eps),
  *     y = (x - mean) * rstd * w + b
+ * in FP32 (so |x - mean| stays below some 1e18, the root of its range).
  *   x     : [R,C] input;  w, b : contiguous [C] of type w_type, either may be
  *           NULL (1 and 0)
  *   y     : [R,C] output, rounded once from FP32
@@ -486,7 +488,8 @@ tri_attn_status tri_act8_unpack(const tri_act8_args *args, tri_attn_stream_t str
  *             overlap.  Elements of a padded row past Nk are left as they were;
  *             those of base in the same 16 bytes as the row's last key are read
  *             (and not used), so they must exist.
- * Sizes: 1 <= B, H, Nq, Nk, with B * Nq * ceil(Nk/8) < 2^31 and H <= 4096. */
+ * Sizes: 1 <= B, H, Nq, Nk, with Nq, Nk <= 2^30, B * Nq * ceil(Nk/8) < 2^31
+ * and H <= 4096. */
 typedef struct {
     int B, H, Nq, Nk, E, table_type;
     const void *table;

@@ -143,6 +143,10 @@ def test_workspace_bytes(lib):
 
 def test_python_refusals_on_cpu(lib):
     x = torch.zeros(4, 128, dtype=BF)
+    for scalar in (lambda t: T.norm_forward(t), lambda t: T.act8_pack(t), lambda t: T.layer_norm(t)):
+        with pytest.raises(Bd.TriAttnError) as e:
+            scalar(torch.tensor(1.0))
+        assert e.value.status == Bd.TRI_ATTN_ERR_SHAPE
     for call in (lambda: T.norm_forward(x), lambda: T.act8_pack(x), lambda: T.layer_norm(x)):
         with pytest.raises(Bd.TriAttnError, match="CUDA device"):
             call()
@@ -539,6 +543,21 @@ def test_norm_linear():
         T.norm_linear(*ts).backward(up)
         for t, c in zip(ts, g8):
             assert (t.grad is None) if not t.requires_grad else torch.equal(t.grad, c)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_norm_linear_under_autocast(dtype):
+    """The projection's dtype sets the result's, in both passes, whatever autocast says."""
+    x = make(40, 128, BF, 6).clone().requires_grad_()
+    p = (make(32, 128, F32, 7) / 11).to(dtype).requires_grad_()
+    T.norm_linear(x, None, None, p).float().square().sum().backward()
+    want, x.grad, dp, p.grad = x.grad, None, p.grad, None
+    with torch.autocast("cuda", dtype=BF):
+        out = T.norm_linear(x, None, None, p)
+        assert out.dtype == dtype
+        out.float().square().sum().backward()
+    assert torch.equal(x.grad, want) and torch.equal(p.grad, dp)
 
 
 @pytest.mark.gpu

@@ -64,7 +64,8 @@ def fake():
 
 FWD_REFUSALS = [
     ({"B": 0}, Bd.TRI_ATTN_ERR_SHAPE), ({"H": 0}, Bd.TRI_ATTN_ERR_SHAPE), ({"Nq": 0}, Bd.TRI_ATTN_ERR_SHAPE),
-    ({"Nk": -8}, Bd.TRI_ATTN_ERR_SHAPE), ({"E": 0}, Bd.TRI_ATTN_ERR_SHAPE), ({"E": 511}, Bd.TRI_ATTN_ERR_UNSUPPORTED),
+    ({"Nk": -8}, Bd.TRI_ATTN_ERR_SHAPE), ({"B": 1, "Nk": 8, "Nq": 2 ** 30 + 1}, Bd.TRI_ATTN_ERR_SHAPE),
+    ({"B": 1, "Nq": 1, "Nk": 2 ** 30 + 1}, Bd.TRI_ATTN_ERR_SHAPE), ({"E": 0}, Bd.TRI_ATTN_ERR_SHAPE), ({"E": 511}, Bd.TRI_ATTN_ERR_UNSUPPORTED),
     ({"H": 4097}, Bd.TRI_ATTN_ERR_UNSUPPORTED), ({"B": 2 ** 20, "Nq": 2 ** 11}, Bd.TRI_ATTN_ERR_SHAPE),
     ({"edges": None}, Bd.TRI_ATTN_ERR_NULL), ({"pos_q": None}, Bd.TRI_ATTN_ERR_NULL),
     ({"group_k": None}, Bd.TRI_ATTN_ERR_NULL), ({"table": None}, Bd.TRI_ATTN_ERR_NULL),
@@ -131,14 +132,30 @@ def test_python_refusals_on_cpu(lib):
         T.relpos_forward(t, e, pos, pos)
     for args, want in (((t[:6], e, pos, pos), Bd.TRI_ATTN_ERR_SHAPE), ((t, e, pos.long(), pos), Bd.TRI_ATTN_ERR_DTYPE),
                        ((t, e.long(), pos, pos), Bd.TRI_ATTN_ERR_DTYPE), ((t.half(), e, pos, pos), Bd.TRI_ATTN_ERR_DTYPE),
+                       ((t[0], e, pos, pos), Bd.TRI_ATTN_ERR_SHAPE), ((t, e, pos, pos, None, None, t), Bd.TRI_ATTN_ERR_SHAPE),
+                       ((t, e, torch.zeros(2, 8, dtype=I32), torch.zeros(3, 8, dtype=I32)), Bd.TRI_ATTN_ERR_SHAPE),
                        ((t, e, pos, pos, pos, pos), Bd.TRI_ATTN_ERR_SHAPE), ((t, e, pos, pos, pos), Bd.TRI_ATTN_ERR_NULL),
                        ((t, e, pos, pos, None, None, torch.zeros(1, 4, 8, 16, dtype=BF)), Bd.TRI_ATTN_ERR_SHAPE)):
         with pytest.raises(Bd.TriAttnError) as err:
             T.relpos_forward(*args)
         assert err.value.status == want
-    with pytest.raises(Bd.TriAttnError) as err:
-        T.relpos_backward(torch.zeros(1, 4, 8, 9, dtype=BF), e, pos, pos)
-    assert err.value.status == Bd.TRI_ATTN_ERR_SHAPE
+    for d in (torch.zeros(1, 4, 8, 9, dtype=BF), torch.zeros(4, 8, 8, dtype=BF)):
+        with pytest.raises(Bd.TriAttnError) as err:
+            T.relpos_backward(d, e, pos, pos)
+        assert err.value.status == Bd.TRI_ATTN_ERR_SHAPE
+
+
+def test_rows_that_end_with_their_storage_are_copied():
+    """Odd rows whose last 16 bytes reach past the storage are not handed to the kernels as they are."""
+    full = torch.zeros(2 * 16, dtype=BF)
+    view = full.as_strided((1, 1, 2, 13), (32, 32, 16, 1))
+    assert T.relpos._layout(view).data_ptr() == view.data_ptr()
+    short = torch.empty(16 + 13, dtype=BF).as_strided((1, 1, 2, 13), (32, 32, 16, 1))
+    if short.data_ptr() % 16 == 0:
+        assert T.relpos._layout(short).data_ptr() != short.data_ptr()
+    assert T.relpos._layout(full.as_strided((1, 1, 2, 16), (32, 32, 16, 1))).data_ptr() == full.data_ptr()
+    odd = torch.zeros(1, 1, 4, 13, dtype=BF)  # rows at odd elements
+    assert T.relpos._layout(odd).stride(2) == 16
 
 
 # ---------------------------------------------------------------------------

@@ -389,11 +389,11 @@ const char* tri_attn_strerror(tri_attn_status s) {
     switch (s) {
         case TRI_ATTN_OK: return "ok";
         case TRI_ATTN_ERR_NULL: return "a required pointer is NULL";
-        case TRI_ATTN_ERR_SHAPE: return "B, N or H out of range";
-        case TRI_ATTN_ERR_STRIDE: return "innermost stride must be 1 and other strides non-negative multiples of 8 elements";
-        case TRI_ATTN_ERR_ALIGN: return "a data pointer is not 16-byte aligned";
+        case TRI_ATTN_ERR_SHAPE: return "a size is out of range";
+        case TRI_ATTN_ERR_STRIDE: return "innermost stride must be 1 and the others as the call takes them (attention: non-negative multiples of 8 elements)";
+        case TRI_ATTN_ERR_ALIGN: return "a data pointer is not aligned as the call asks (attention: 16 bytes)";
         case TRI_ATTN_ERR_DTYPE: return "wrong element type";
-        case TRI_ATTN_ERR_UNSUPPORTED: return "unsupported size (d must be 32 or 64, N <= 4096)";
+        case TRI_ATTN_ERR_UNSUPPORTED: return "unsupported size or option (attention: d must be 32 or 64, N <= 4096)";
         case TRI_ATTN_ERR_WORKSPACE: return "workspace missing or too small";
         case TRI_ATTN_ERR_ARCH: return "current device is not compute capability 10.0 (sm_100)";
         case TRI_ATTN_ERR_CUDA: return "a CUDA call failed";

@@ -223,7 +223,8 @@ tri_attn_status act8_impl(const tri_act8_args* a, bool pack, tri_attn_stream_t s
 // relative position bias
 // ---------------------------------------------------------------------------
 tri_attn_status check_relpos_sizes(int B, int H, int Nq, int Nk, int E) {
-    if (B < 1 || H < 1 || Nq < 1 || Nk < 1 || E < 1) return TRI_ATTN_ERR_SHAPE;
+    constexpr int kMost = 1 << 30;  // row and key numbers plus a step stay within 32 bits
+    if (B < 1 || H < 1 || Nq < 1 || Nk < 1 || E < 1 || Nq > kMost || Nk > kMost) return TRI_ATTN_ERR_SHAPE;
     if (static_cast<double>(B) * Nq * ((static_cast<int64_t>(Nk) + 7) / 8) >= 2147483648.0) return TRI_ATTN_ERR_SHAPE;
     return H > 4096 || E > tri::kRelMaxEdges ? TRI_ATTN_ERR_UNSUPPORTED : TRI_ATTN_OK;
 }

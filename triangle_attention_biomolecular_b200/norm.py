@@ -86,8 +86,10 @@ def _empty8(x: torch.Tensor, kind: str):
 
 def act8_pack(x: torch.Tensor, kind: str = "int8") -> Act8:
     """x (BF16 or FP32, [..., C]) in 8 bits."""
+    x2 = _rows(x)
+    B._rows(x2, "x")
     a = _empty8(x, kind)
-    B.tri_act8_pack(_rows(x), a.codes, a.exps, a.kind)
+    B.tri_act8_pack(x2, a.codes, a.exps, a.kind)
     return a
 
 
@@ -191,18 +193,25 @@ def layer_norm(x, weight=None, bias=None, eps: float = 1e-5, out_dtype: Optional
     return LayerNormFunction.apply(x, weight, bias, eps, out_dtype, checkpoint)
 
 
+def _product(a, b):
+    """a @ b in their own dtype, whatever an autocast around the call says."""
+    with torch.autocast(a.device.type, enabled=False):
+        return torch.matmul(a, b)
+
+
 class NormLinearFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, proj, eps, checkpoint):
         y, stats, kept = norm_forward(x, weight, bias, eps, proj.dtype, checkpoint)
         _save(ctx, x, kept, stats, weight, bias, proj)
         ctx.eps = eps
-        return torch.matmul(y, proj.t())
+        return _product(y, proj.t())
 
     @staticmethod
     @once_differentiable
     def backward(ctx, g):
         x, stats, weight, bias, proj = _saved(ctx)
+        g = g.to(proj.dtype)
         need = ctx.needs_input_grad
         dx = dw = db = dproj = None
         if need[3]:
@@ -210,9 +219,9 @@ class NormLinearFunction(torch.autograd.Function):
                 y = norm_restore(x, stats, weight, bias, proj.dtype)
             else:
                 y = norm_forward(x, weight, bias, ctx.eps, proj.dtype)[0]
-            dproj = torch.matmul(g.reshape(-1, g.shape[-1]).t(), y.view(-1, y.shape[-1]))
+            dproj = _product(g.reshape(-1, g.shape[-1]).t(), y.view(-1, y.shape[-1]))
         if need[0] or need[1] or need[2]:
-            dx, dw, db = norm_backward(x, stats, torch.matmul(g, proj), weight, need[0], need[1] or need[2])
+            dx, dw, db = norm_backward(x, stats, _product(g, proj), weight, need[0], need[1] or need[2])
         return (dx, _like(dw, weight) if need[1] else None, _like(db, bias) if need[2] else None, dproj, None, None)
 
 

@@ -103,6 +103,10 @@ def _index(pos_q, pos_k, group_q, group_k, like=None):
 def relpos_forward(table, edges, pos_q, pos_k, group_q=None, group_k=None, base=None):
     """The bias, BF16 [B, H, Nq, Nk] with rows padded to a multiple of 8 elements.  table BF16 or
     FP32 [buckets, H]; positions and groups int32 [N] or [B, N]; base BF16 [B, H, Nq, Nk]."""
+    if table.dim() != 2:
+        raise B.TriAttnError(B.TRI_ATTN_ERR_SHAPE, f"table must be [buckets, H], got {list(table.shape)}")
+    if base is not None and base.dim() != 4:
+        raise B.TriAttnError(B.TRI_ATTN_ERR_SHAPE, f"base must be [B, H, Nq, Nk], got {list(base.shape)}")
     q, k, gq, gk = _index(pos_q, pos_k, group_q, group_k, base)
     bias = _padded((q.shape[0], table.shape[1], q.shape[1], k.shape[1]), table)
     B.tri_relpos_fwd(table.contiguous(), edges, q, k, gq, gk, None if base is None else _layout(base), bias)
@@ -111,6 +115,8 @@ def relpos_forward(table, edges, pos_q, pos_k, group_q=None, group_k=None, base=
 
 def relpos_backward(dbias, edges, pos_q, pos_k, group_q=None, group_k=None):
     """The table's gradient, FP32 [buckets, H], for the bias's gradient (BF16 [B, H, Nq, Nk])."""
+    if dbias.dim() != 4:
+        raise B.TriAttnError(B.TRI_ATTN_ERR_SHAPE, f"dbias must be [B, H, Nq, Nk], got {list(dbias.shape)}")
     q, k, gq, gk = _index(pos_q, pos_k, group_q, group_k, dbias)
     E, H = edges.shape[0], dbias.shape[1]
     dtable = dbias.new_empty((E + 1 + (gq is not None), H), dtype=torch.float32)
