@@ -292,7 +292,7 @@ RelposBwdShape relpos_bwd_shape(int B, int H, int Nq, int Nk, int nb) {
     const int64_t batches = (Nq + tri::kRelRows - 1) / tri::kRelRows;
     s.row_tasks = static_cast<int>(std::min(want, batches));
     s.run = static_cast<int>(std::min<int64_t>(2, batches / s.row_tasks));
-    const int64_t tasks = tiles * s.row_tasks;
+    const int64_t tasks = tiles * s.row_tasks;  // < 2^31: at most one per warp at once, or B * chunks of them
     s.grid = static_cast<unsigned>(std::min<int64_t>((tasks + s.warps - 1) / s.warps, 148 * tri::kRelBwdBlocks));
     return s;
 }

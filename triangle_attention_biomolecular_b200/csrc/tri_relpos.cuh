@@ -195,11 +195,10 @@ __global__ void __launch_bounds__(kRelThreads, kRelFwdBlocks)
     bucket.init(sh_edges, sh_lut, p);  // ends with a barrier: the table is in place too
 
     // the grid holds at least one row of chunks (see the launch)
-    const int64_t id = static_cast<int64_t>(blockIdx.x) * kRelThreads + threadIdx.x;
-    const int rstep = static_cast<int>(static_cast<int64_t>(gridDim.x) * kRelThreads / p.chunks);
-    const int row0 = static_cast<int>(id / p.chunks);
+    const uint32_t id = blockIdx.x * kRelThreads + threadIdx.x, chunks = p.chunks;
+    const int rstep = static_cast<int>(gridDim.x * kRelThreads / chunks), row0 = static_cast<int>(id / chunks);
     if (row0 >= rstep) return;  // no barrier follows
-    const int j0 = static_cast<int>(id - static_cast<int64_t>(row0) * p.chunks) * 8, nj = min(8, p.Nk - j0);
+    const int j0 = static_cast<int>(id - row0 * chunks) * 8, nj = min(8, p.Nk - j0);
     int key[8], pmin = 0, pmax = 0, g0 = 0;
     bool one_group = true;
     const int32_t* gk = nullptr;
@@ -405,14 +404,12 @@ __global__ void __launch_bounds__(kRelBwdWarps * 32, kRelBwdBlocks) tri_relpos_b
     const int h0 = blockIdx.y * Hc, h = h0 + lane / S, sub = lane % S;
     const int tiles = (p.chunks + S - 1) / S;
     float* mine = sums + static_cast<size_t>(warp) * p.nb * 32 + lane;
-    const int64_t tasks = static_cast<int64_t>(p.B) * tiles * p.row_tasks;
-    for (int64_t task = static_cast<int64_t>(blockIdx.x) * warps + warp; task < tasks;
-         task += static_cast<int64_t>(gridDim.x) * warps) {
+    const uint32_t tasks = static_cast<uint32_t>(p.B) * tiles * p.row_tasks;  // < 2^31, see the launch
+    for (uint32_t task = blockIdx.x * warps + warp; task < tasks; task += gridDim.x * warps) {
         // neighbouring warps take neighbouring keys of the same rows
-        const int tile = static_cast<int>(task % tiles);
-        const int64_t br = task / tiles;
-        const int rt = static_cast<int>(br % p.row_tasks), b = static_cast<int>(br / p.row_tasks);
-        const int c = tile * S + sub;
+        const uint32_t br = task / tiles, tile = task - br * tiles;
+        const int b = static_cast<int>(br / p.row_tasks), rt = static_cast<int>(br - b * p.row_tasks);
+        const int c = static_cast<int>(tile) * S + sub;
         if (c >= p.chunks || h >= p.H) continue;  // no barrier or warp-wide step inside the walk
         const int j0 = c * 8, nj = min(8, p.Nk - j0);
         const int32_t* keys = p.pos_k + b * p.ks + j0;
