@@ -552,24 +552,28 @@ __global__ void __launch_bounds__(kRelBwdWarps * 32, kRelBwdBlocks) tri_relpos_b
         if (GROUPS) mine[(p.E + 1) * 32] += apart;
     }
     __syncthreads();
-    // the block's sums: a warp per bucket, over the warps, then over the chunks side by side
-    float* out = p.partial + static_cast<int64_t>(blockIdx.x) * p.nb * p.H;
-#pragma unroll 4
-    for (int k = warp; k < p.nb; k += warps) {
+    // the block's sums: word by word over the warps, then over the chunks side by side, starting
+    // at another chunk for each bucket so that the lanes read different banks
+    const int words = p.nb * 32;
+#pragma unroll 3
+    for (int x = threadIdx.x; x < words; x += blockDim.x) {
         float s[kRelBwdWarps];
 #pragma unroll
-        for (int w = 0; w < kRelBwdWarps; ++w)
-            s[w] = w < warps ? sums[(static_cast<size_t>(w) * p.nb + k) * 32 + lane] : 0.f;
+        for (int w = 0; w < kRelBwdWarps; ++w) s[w] = w < warps ? sums[w * words + x] : 0.f;
 #pragma unroll
         for (int m = 1; m < kRelBwdWarps; m *= 2)
 #pragma unroll
             for (int w = 0; w < kRelBwdWarps; w += 2 * m) s[w] += s[w + m];
-#pragma unroll
-        for (int m = 1; m < 32; m *= 2) {
-            const float other = __shfl_xor_sync(0xFFFFFFFFu, s[0], m);
-            if (m < S) s[0] += other;
-        }
-        if (sub == 0 && h < p.H && !dead) out[static_cast<int64_t>(k) * p.H + h] = s[0];
+        sums[x] = s[0];
+    }
+    __syncthreads();
+    float* out = p.partial + static_cast<int64_t>(blockIdx.x) * p.nb * p.H + h0;
+    for (int x = threadIdx.x; x < p.nb * Hc; x += blockDim.x) {
+        const int k = x / Hc, hh = x & (Hc - 1);
+        float s = 0.f;
+#pragma unroll 8
+        for (int q = 0; q < S; ++q) s += sums[k * 32 + hh * S + ((q + k) & (S - 1))];
+        if (h0 + hh < p.H && !dead) out[static_cast<int64_t>(k) * p.H + hh] = s;
     }
 }
 
