@@ -149,7 +149,7 @@ tri_attn_status norm_fwd_impl(const tri_norm_fwd_args* a, bool restore, tri_attn
     NormParams p{};
     norm_params(p, *a, s);
     const unsigned grid = static_cast<unsigned>(
-        std::min<int64_t>((a->R + s.per_block - 1) / s.per_block, 148 * (s.lanes > 32 ? 8 : vec ? tri::kNormFwdBlocks : tri::kNormFwdBlocksBy)));
+        std::min<int64_t>((a->R + s.per_block - 1) / s.per_block, 148 * (s.lanes > 32 ? 8 : tri::norm_fwd_blocks(vec, !restore && xe == 4))));
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     with_mode(vec, s.lanes, [&](auto m, auto wd) {
         constexpr int MODE = decltype(m)::value;

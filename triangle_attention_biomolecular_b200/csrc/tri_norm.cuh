@@ -377,8 +377,10 @@ struct NormRow8 {
 // ---------------------------------------------------------------------------
 constexpr int kNormThreads = 256;   // rows of up to 512 channels: 256 / G of them per block
 constexpr int kNormMaxWarps = 16;   // rows of up to 8192 channels: one block, a warp per 512
-// blocks per SM; the element-wise rows hold sixteen addresses' worth of registers more
-constexpr int kNormFwdBlocks = 4, kNormFwdBlocksBy = 3, kNormBwdBlocks = 2;
+// Blocks per SM.  A row on its way takes eight registers in BF16 and sixteen in FP32 or element by
+// element, so those get the registers of a block less.
+constexpr int kNormBwdBlocks = 2;
+__host__ __device__ constexpr int norm_fwd_blocks(bool vec, bool f32) { return vec && !f32 ? 4 : 3; }
 
 // Sums over the G lanes of this lane's row, the same bits in every lane.  Rows
 // of more than one warp meet in shared memory; `turn` alternates between two
@@ -416,7 +418,7 @@ __device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
 // forward; with RESTORE the row comes from its 8-bit form and its statistics
 // ---------------------------------------------------------------------------
 template <typename TX, typename TY, int ACT, int MODE, bool RESTORE, bool WIDE>
-__global__ void __launch_bounds__(WIDE ? 32 * kNormMaxWarps : kNormThreads, WIDE ? 1 : MODE == kVec ? kNormFwdBlocks : kNormFwdBlocksBy)
+__global__ void __launch_bounds__(WIDE ? 32 * kNormMaxWarps : kNormThreads, WIDE ? 1 : norm_fwd_blocks(MODE == kVec, sizeof(TX) == 4 && !RESTORE))
     tri_norm_fwd_kernel(const __grid_constant__ NormParams p) {
     __shared__ float2 red[2][kNormMaxWarps];
     __shared__ __align__(16) float sh_w[WIDE ? 4 : 512], sh_b[WIDE ? 4 : 512];
