@@ -11,6 +11,13 @@
 // The 8-bit form shares a power-of-two scale between 32 neighbouring channels.
 // With such a scale value / scale and code * scale are exact, so a code depends
 // on one rounding only and BF16 restores it without another.
+//
+// Measured at 768 x 768 rows of 128 channels, in bytes that must move over time
+// (6.57 TB/s is the card's copy rate): forward FP32 to BF16 72 us, 6.4 TB/s; its
+// backward 116 us, 6.6 TB/s; forward BF16 with the int8 form 65 us, 5.9 TB/s;
+// restore 45 us, 5.2 TB/s; backward from the int8 form 76 us, 5.1 TB/s; these
+// last two issue the most instructions per byte.  A second row on its way per
+// lane gained nothing (the BF16 backward spilled: 22 to 27 us at 384 x 384 rows).
 #pragma once
 
 #include <cuda_fp8.h>
@@ -658,7 +665,11 @@ __global__ void __launch_bounds__(1024) tri_ordered_sum_kernel(const float* __re
 // an activation into and out of its 8-bit form
 // ---------------------------------------------------------------------------
 // The lanes share a row as in the norm; rows of more than 512 channels are cut
-// into pieces of 512, a warp each.  What hides the latency here is many warps.
+// into pieces of 512, a warp each.  What hides the latency here is many warps: with
+// a row loaded ahead, for which two blocks per SM less fit, 640 x 640 rows of 128
+// BF16 channels packed in 36 us instead of 31 (5.2 TB/s; unpacking 27 us, 5.9 TB/s).
+// Element by element, 20011 rows of 209 FP32 channels take 13 and 8 us, bound by
+// latency: each warp has two rows.
 constexpr int kAct8Blocks = 6, kAct8BlocksBy = 4;  // per SM
 template <typename TX, int ACT, int MODE, bool PACK>
 __global__ void __launch_bounds__(kNormThreads, MODE == kVec ? kAct8Blocks : kAct8BlocksBy)
