@@ -14,7 +14,7 @@
 //
 // Measured at 768 x 768 rows of 128 channels, in bytes that must move over time
 // (6.57 TB/s is the card's copy rate): forward FP32 to BF16 72 us, 6.4 TB/s; its
-// backward 116 us, 6.6 TB/s; forward BF16 with the int8 form 65 us, 5.9 TB/s;
+// backward 115 us, 6.6 TB/s; forward BF16 with the int8 form 64 us, 6.0 TB/s;
 // restore 45 us, 5.2 TB/s; backward from the int8 form 76 us, 5.1 TB/s; these
 // last two issue the most instructions per byte.  A second row on its way per
 // lane gained nothing (the BF16 backward spilled: 22 to 27 us at 384 x 384 rows).
@@ -244,24 +244,46 @@ __device__ __forceinline__ float act8_value(uint32_t byte) {
 
 // values of four codes in a word, times the scale
 template <int ACT>
-__device__ __forceinline__ void act8_value4(uint32_t w, float scale, float* v) {
+__device__ __forceinline__ void act8_value4(uint32_t w, float scale, float2* v) {
+    const float2 s = make_float2(scale, scale);
     if constexpr (ACT == ACT_INT8) {
         // byte b of (w ^ 0x80808080) in the low bits of 2^23 is 2^23 + 128 + code
         const uint32_t u = w ^ 0x80808080u;
+        const float2 off = make_float2(-8388736.f, -8388736.f);
 #pragma unroll
-        for (int k = 0; k < 4; ++k)
-            v[k] = (__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440u + k)) - 8388736.f) * scale;
+        for (int k = 0; k < 2; ++k)
+            v[k] = fmul2(fadd2(make_float2(__uint_as_float(__byte_perm(u, 0x4B000000u, 0x7440u + 2 * k)),
+                                           __uint_as_float(__byte_perm(u, 0x4B000000u, 0x7441u + 2 * k))),
+                               off),
+                         s);
     } else {
         uint32_t h0, h1;
         asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h0) : "h"(static_cast<uint16_t>(w & 0xFFFFu)));
         asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h1) : "h"(static_cast<uint16_t>(w >> 16)));
-        const float2 a = __half22float2(*reinterpret_cast<__half2*>(&h0));
-        const float2 b = __half22float2(*reinterpret_cast<__half2*>(&h1));
-        v[0] = a.x * scale;
-        v[1] = a.y * scale;
-        v[2] = b.x * scale;
-        v[3] = b.y * scale;
+        v[0] = fmul2(__half22float2(*reinterpret_cast<__half2*>(&h0)), s);
+        v[1] = fmul2(__half22float2(*reinterpret_cast<__half2*>(&h1)), s);
     }
+}
+// four codes in a word
+template <int ACT>
+__device__ __forceinline__ uint32_t act8_code4(float2 a, float2 b, float inv) {
+    const float2 s = make_float2(inv, inv);
+    if constexpr (ACT == ACT_INT8) {
+        const float2 m = make_float2(12582912.f, 12582912.f);  // as in act8_code2
+        a = ffma2(a, s, m);
+        b = ffma2(b, s, m);
+        const uint32_t lo = __byte_perm(__float_as_uint(a.x), __float_as_uint(a.y), 0x0040);
+        const uint32_t hi = __byte_perm(__float_as_uint(b.x), __float_as_uint(b.y), 0x0040);
+        return __byte_perm(lo, hi, 0x5410);
+    } else {
+        return act8_code2<ACT>(a.x, a.y, inv) | act8_code2<ACT>(b.x, b.y, inv) << 16;
+    }
+}
+// the larger magnitude of three; a NaN stays one
+__device__ __forceinline__ float absmax3(float a, float b, float c) {
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
 }
 
 // this lane's sixteen channels, from channel c0 of their row on, into its 8-bit form; every lane of
@@ -272,16 +294,11 @@ __device__ __forceinline__ void act8_emit(const NormParams& p, int64_t row, bool
     const int C = p.C - c0;
     uint8_t* codes = p.codes + row * p.cs + c0;
     uint8_t* exps = p.exps + row * p.es + c0 / 32;
-    float v[16];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-        v[2 * k] = u[k].x;
-        v[2 * k + 1] = u[k].y;
-    }
     if constexpr (MODE == kVec) {
-        uint32_t a = 0;
+        float m = 0.f;
 #pragma unroll
-        for (int k = 0; k < 16; ++k) a = max(a, __float_as_uint(v[k]) & 0x7FFFFFFFu);
+        for (int k = 0; k < 8; ++k) m = absmax3(m, u[k].x, u[k].y);
+        uint32_t a = __float_as_uint(m) & 0x7FFFFFFFu;
         const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, a, 1);
         if (G > 1) a = max(a, other);  // two lanes share a block (C = 16: one lane is the row)
         const uint32_t eb = act8_exp<ACT>(a);
@@ -289,7 +306,7 @@ __device__ __forceinline__ void act8_emit(const NormParams& p, int64_t row, bool
         uint32_t w[4];
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            w[q] = act8_code2<ACT>(v[4 * q], v[4 * q + 1], inv) | act8_code2<ACT>(v[4 * q + 2], v[4 * q + 3], inv) << 16;
+            w[q] = act8_code4<ACT>(u[2 * q], u[2 * q + 1], inv);
             if (eb == 255u) w[q] = 0u;
         }
         if (ok && g * 16 < C) {
@@ -297,7 +314,10 @@ __device__ __forceinline__ void act8_emit(const NormParams& p, int64_t row, bool
             if ((g & 1) == 0) exps[g >> 1] = static_cast<uint8_t>(eb);
         }
     } else {
+        float v[16];
         uint32_t a[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) v[k] = k & 1 ? u[k / 2].y : u[k / 2].x;
 #pragma unroll
         for (int k = 0; k < 16; ++k) a[k] = __float_as_uint(v[k]) & 0x7FFFFFFFu;
         if constexpr (MODE == kBy32) {
@@ -361,11 +381,8 @@ struct NormRow8 {
     __device__ __forceinline__ void values(float2 (&v)[8]) const {
         if constexpr (MODE == kVec) {
             const float s = act8_scale(e[0]);
-            float u[16];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) act8_value4<ACT>(w[q], s, u + 4 * q);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = make_float2(u[2 * k], u[2 * k + 1]);
+            for (int q = 0; q < 4; ++q) act8_value4<ACT>(w[q], s, v + 2 * q);
         } else {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
