@@ -48,7 +48,8 @@ struct NormParams {
     int64_t dys;
     void* dx;
     int64_t dxs;
-    float* partial;  // [gridDim.x][2][C], or NULL
+    float* partial;  // [gridDim.x][2][C], or NULL; a single block writes dw and db themselves
+    float *dw, *db;
 };
 
 // ---------------------------------------------------------------------------
@@ -611,14 +612,15 @@ __global__ void __launch_bounds__(WIDE ? 32 * kNormMaxWarps : kNormThreads, WIDE
         }
     }
     if (!p.partial) return;  // the same for every thread
-    float* out = p.partial + static_cast<int64_t>(blockIdx.x) * 2 * p.C;
+    float* out_w = gridDim.x == 1 ? p.dw : p.partial + static_cast<int64_t>(blockIdx.x) * 2 * p.C;
+    float* out_b = gridDim.x == 1 ? p.db : out_w + p.C;
     if constexpr (WIDE) {
 #pragma unroll
         for (int k = 0; k < 16; ++k) {
             const int c = norm_col<MODE>(g, k);
             if (c < p.C && !dead) {
-                out[c] = k & 1 ? dw[k / 2].y : dw[k / 2].x;
-                out[p.C + c] = k & 1 ? db[k / 2].y : db[k / 2].x;
+                out_w[c] = k & 1 ? dw[k / 2].y : dw[k / 2].x;
+                out_b[c] = k & 1 ? db[k / 2].y : db[k / 2].x;
             }
         }
     } else {
@@ -646,7 +648,7 @@ __global__ void __launch_bounds__(WIDE ? 32 * kNormMaxWarps : kNormThreads, WIDE
             float s = 0.f;
 #pragma unroll
             for (int q = 0; q < kNormThreads / 32; ++q) s += sums[q][which][col];
-            if (!dead) out[c] = s;
+            if (!dead) (which ? out_b : out_w)[col] = s;
         }
     }
 }
