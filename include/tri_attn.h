@@ -457,7 +457,7 @@ size_t tri_norm_bwd_workspace_bytes(int64_t R, int C);
 tri_attn_status tri_norm_bwd(const tri_norm_bwd_args *args, tri_attn_stream_t stream);
 
 /* Pack: act = x in 8 bits.  Unpack: x = the values act stands for, rounded to
- * x_type.  x is [R,C] of type x_type; any C >= 1. */
+ * x_type.  x is [R,C] of type x_type; 1 <= C <= 2^30. */
 typedef struct {
     int64_t R;
     void *x;

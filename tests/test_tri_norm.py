@@ -121,6 +121,7 @@ def test_restore_and_act8_refusals(lib):
     assert lib.tri_act8_pack(None, None) == lib.tri_act8_unpack(None, None) == Bd.TRI_ATTN_ERR_NULL
     for fn, what, want in (
             (lib.tri_act8_pack, {"R": -1}, Bd.TRI_ATTN_ERR_SHAPE), (lib.tri_act8_pack, {"C": 0}, Bd.TRI_ATTN_ERR_SHAPE),
+            (lib.tri_act8_unpack, {"C": 2 ** 30 + 1}, Bd.TRI_ATTN_ERR_SHAPE),
             (lib.tri_act8_pack, {"x": None}, Bd.TRI_ATTN_ERR_NULL), (lib.tri_act8_pack, {"x_type": 5}, Bd.TRI_ATTN_ERR_DTYPE),
             (lib.tri_act8_pack, {"act__codes_stride": 127}, Bd.TRI_ATTN_ERR_STRIDE),  # code rows would overlap
             (lib.tri_act8_pack, {"act__exps": None}, Bd.TRI_ATTN_ERR_NULL),
@@ -279,6 +280,28 @@ def test_long_sums_and_only_some_gradients():
     assert none is None and torch.equal(dw, dw2) and torch.equal(db, db2)
     dx3, dw3, db3 = T.norm_backward(x, stats, dy, w, need_dw=False)
     assert dw3 is None and db3 is None and torch.equal(dx, dx3)
+
+
+@pytest.mark.gpu
+def test_large_rows_past_32_bits():
+    """Element offsets past 2^31: the last rows equal the same rows alone, in every direction."""
+    R, C = 2 ** 24 + 77, 128
+    x = torch.empty(R, C, dtype=BF, device="cuda").normal_(generator=torch.Generator("cuda").manual_seed(3))
+    w, b = 1 + 0.3 * make(1, C, F32, 1)[0], make(1, C, F32, 2)[0]
+    y, stats, a = T.norm_forward(x, w, b, checkpoint="int8")
+    again = T.norm_restore(a, stats, w, b)
+    dx, dw, db = T.norm_backward(a, stats, y, w)
+    tail = slice(R - 500, R)
+    y1, s1, a1 = T.norm_forward(x[tail], w, b, checkpoint="int8")
+    assert torch.equal(y[tail], y1) and torch.equal(stats[:, tail], s1)
+    assert torch.equal(a.codes[tail], a1.codes) and torch.equal(a.exps[tail], a1.exps)
+    assert torch.equal(again[tail], T.norm_restore(a1, s1, w, b))
+    assert torch.equal(dx[tail], T.norm_backward(a1, s1, y1, w)[0])
+    assert torch.equal(T.act8_unpack(a)[tail], T.act8_unpack(a1))
+    # db: a thread adds R / (296 x 32) < 1800 rows, then < 64 partial sums
+    want = torch.stack([c.double().sum(0) for c in y.split(2 ** 21)]).sum(0)
+    size = torch.stack([c.double().abs().sum(0) for c in y.split(2 ** 21)]).sum(0)
+    assert ((db.double() - want).abs() <= 1900 * U * size).all() and torch.isfinite(dw).all()
 
 
 @pytest.mark.gpu

@@ -145,6 +145,17 @@ def test_python_refusals_on_cpu(lib):
         assert err.value.status == Bd.TRI_ATTN_ERR_SHAPE
 
 
+def test_a_bias_of_another_dtype_is_refused_and_not_cast(lib):
+    pos, e = torch.arange(9, dtype=I32), T.relpos_edges_clipped(3, "cpu")
+    for n in (8, 9):
+        d = torch.zeros(1, 4, n, n)
+        for call in (lambda: T.relpos_backward(d, e, pos[:n], pos[:n]),
+                     lambda: T.relpos_forward(torch.zeros(7, 4), e, pos[:n], pos[:n], base=d)):
+            with pytest.raises(Bd.TriAttnError) as err:
+                call()
+            assert err.value.status == Bd.TRI_ATTN_ERR_DTYPE
+
+
 def test_rows_that_end_with_their_storage_are_copied():
     """Odd rows whose last 16 bytes reach past the storage are not handed to the kernels as they are."""
     full = torch.zeros(2 * 16, dtype=BF)
@@ -226,6 +237,19 @@ def test_parity(case):
     tol = (8 * 515 + 131) * U * O.relpos_bwd(np.abs(D), k, table.shape[0])
     assert np.all(np.abs(f64(dt) - O.relpos_bwd(D, k, table.shape[0])) <= tol)
     assert torch.equal(dt, T.relpos_backward(d, e, pq, pk, gq, gk))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [3, 20, 41, 64, 71, 130])
+@pytest.mark.parametrize("H", [1, 2, 5, 8, 33])
+def test_small_whole_numbers_are_summed_exactly(N, H):
+    """One block and many, every split of heads: sums of small whole numbers are exact."""
+    g = torch.Generator().manual_seed(N * 40 + H)
+    pos = torch.cumsum(1 + (torch.rand(N, generator=g) < 0.2).int() * 3, 0).int().cuda()
+    d = torch.randint(-8, 9, (1, H, N, (N + 7) // 8 * 8), generator=g).to(BF).cuda()[..., :N]
+    for e in (T.relpos_edges_clipped(4), T.relpos_edges_log(6, 5000)):
+        k = bucket_of(e, pos[None], pos[None], None, None)
+        np.testing.assert_array_equal(f64(T.relpos_backward(d, e, pos, pos)), O.relpos_bwd(f64(d), k, e.numel() + 1))
 
 
 @pytest.mark.gpu

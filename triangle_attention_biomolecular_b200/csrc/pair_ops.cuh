@@ -151,8 +151,8 @@ tri_attn_status norm_fwd_impl(const tri_norm_fwd_args* a, bool restore, tri_attn
     const NormShape s = norm_shape(a->C, vec);
     NormParams p{};
     norm_params(p, *a, s);
-    const unsigned grid = static_cast<unsigned>(
-        std::min<int64_t>((a->R + s.per_block - 1) / s.per_block, 148 * (s.lanes > 32 ? 8 : tri::norm_fwd_blocks(vec, !restore && xe == 4))));
+    const int per_sm = s.lanes > 32 ? 8 : tri::norm_fwd_blocks(vec, !restore && xe == 4);
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>((a->R + s.per_block - 1) / s.per_block, 148 * per_sm));
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     with_mode(vec, s.lanes, [&](auto m, auto wd) {
         constexpr int MODE = decltype(m)::value;
@@ -163,13 +163,15 @@ tri_attn_status norm_fwd_impl(const tri_norm_fwd_args* a, bool restore, tri_attn
             if (restore) {
                 if constexpr (std::is_same<TX, TY>::value)
                     with_kind(a->act.kind, [&](auto k) {
-                        tri::tri_norm_fwd_kernel<TX, TY, decltype(k)::value, MODE, true, WIDE><<<grid, s.threads, 0, cs>>>(p);
+                        tri::tri_norm_fwd_kernel<TX, TY, decltype(k)::value, MODE, true, WIDE>
+                            <<<grid, s.threads, 0, cs>>>(p);
                     });
             } else if (!act) {
                 tri::tri_norm_fwd_kernel<TX, TY, tri::ACT_NONE, MODE, false, WIDE><<<grid, s.threads, 0, cs>>>(p);
             } else {
                 with_kind(a->act.kind, [&](auto k) {
-                    tri::tri_norm_fwd_kernel<TX, TY, decltype(k)::value, MODE, false, WIDE><<<grid, s.threads, 0, cs>>>(p);
+                    tri::tri_norm_fwd_kernel<TX, TY, decltype(k)::value, MODE, false, WIDE>
+                        <<<grid, s.threads, 0, cs>>>(p);
                 });
             }
         });
@@ -183,7 +185,7 @@ tri_attn_status act8_impl(const tri_act8_args* a, bool pack, tri_attn_stream_t s
     const int C = a->C, x_type = a->x_type;
     const tri_act8& act = a->act;
     void* x = a->x;
-    if (R < 0 || R > (int64_t{1} << 40) || C < 1) return TRI_ATTN_ERR_SHAPE;
+    if (R < 0 || R > (int64_t{1} << 40) || C < 1 || C > (1 << 30)) return TRI_ATTN_ERR_SHAPE;
     if (!type_ok(x_type)) return TRI_ATTN_ERR_DTYPE;
     const int64_t xe = type_bytes(x_type);
     tri_attn_status st = check_rows(x, R, C, xs, xe, !pack);
@@ -204,7 +206,8 @@ tri_attn_status act8_impl(const tri_act8_args* a, bool pack, tri_attn_stream_t s
     p.exps = static_cast<uint8_t*>(act.exps);
     p.es = act.exps_stride;
     const int64_t per = tri::kNormThreads / p.lanes, items = R * pieces;
-    const unsigned grid = static_cast<unsigned>(std::min<int64_t>((items + per - 1) / per, 148 * (vec ? tri::kAct8Blocks : tri::kAct8BlocksBy) * 2));
+    const int per_sm = 2 * (vec ? tri::kAct8Blocks : tri::kAct8BlocksBy);
+    const unsigned grid = static_cast<unsigned>(std::min<int64_t>((items + per - 1) / per, 148 * per_sm));
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     with_mode(vec, p.lanes, [&](auto m, auto wd) {
         if constexpr (!decltype(wd)::value)  // pieces are no wider than a warp
@@ -277,7 +280,8 @@ RelposBwdShape relpos_bwd_shape(int B, int H, int Nq, int Nk, int nb) {
     int64_t fewest = INT64_MAX;
     for (int heads = 32; heads >= 1; heads /= 2) {
         const int side = 32 / heads;
-        const int64_t lanes = static_cast<int64_t>((chunks + side - 1) / side) * side * ((H + heads - 1) / heads * heads);
+        const int64_t lanes =
+            static_cast<int64_t>((chunks + side - 1) / side) * side * ((H + heads - 1) / heads * heads);
         if (lanes < fewest && (heads <= 4 || side >= chunks)) {
             fewest = lanes;
             s.heads = heads;
@@ -414,7 +418,8 @@ tri_attn_status tri_relpos_fwd(const tri_relpos_fwd_args* a, tri_attn_stream_t s
     // heads runs on 8 blocks in place of 2)
     while (p.heads > 4 && (items + threads - 1) / threads * ((a->H + p.heads - 1) / p.heads) < 74) p.heads /= 2;
     const unsigned head_blocks = (a->H + p.heads - 1) / p.heads;
-    const int64_t at_once = std::max<int64_t>(148 * tri::kRelFwdBlocks / head_blocks, (p.chunks + threads - 1) / threads);
+    const int64_t at_once =
+        std::max<int64_t>(148 * tri::kRelFwdBlocks / head_blocks, (p.chunks + threads - 1) / threads);
     const dim3 grid(static_cast<unsigned>(std::min((items + threads - 1) / threads, at_once)), head_blocks);
     const size_t smem = tri::relpos_fwd_smem(p.nb, p.heads, p.base != nullptr);
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);

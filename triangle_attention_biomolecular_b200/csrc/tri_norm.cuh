@@ -443,7 +443,8 @@ __device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
 // forward; with RESTORE the row comes from its 8-bit form and its statistics
 // ---------------------------------------------------------------------------
 template <typename TX, typename TY, int ACT, int MODE, bool RESTORE, bool WIDE>
-__global__ void __launch_bounds__(WIDE ? 32 * kNormMaxWarps : kNormThreads, WIDE ? 1 : norm_fwd_blocks(MODE == kVec, sizeof(TX) == 4 && !RESTORE))
+__global__ void __launch_bounds__(WIDE ? 32 * kNormMaxWarps : kNormThreads,
+                                  WIDE ? 1 : norm_fwd_blocks(MODE == kVec, sizeof(TX) == 4 && !RESTORE))
     tri_norm_fwd_kernel(const __grid_constant__ NormParams p) {
     __shared__ float2 red[2][kNormMaxWarps];
     __shared__ __align__(16) float sh_w[WIDE ? 4 : 512], sh_b[WIDE ? 4 : 512];

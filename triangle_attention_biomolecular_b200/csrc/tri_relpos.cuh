@@ -399,7 +399,8 @@ struct RelposBatch {
 };
 
 template <bool GROUPS>
-__global__ void __launch_bounds__(kRelBwdWarps * 32, kRelBwdBlocks) tri_relpos_bwd_kernel(const __grid_constant__ RelposParams p) {
+__global__ void __launch_bounds__(kRelBwdWarps * 32, kRelBwdBlocks)
+    tri_relpos_bwd_kernel(const __grid_constant__ RelposParams p) {
     extern __shared__ __align__(1024) uint8_t smem[];
     grid_dependents_start();
     const bool dead = device_error_pending();

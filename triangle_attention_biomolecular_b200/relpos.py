@@ -54,6 +54,8 @@ def _layout(t: torch.Tensor) -> torch.Tensor:
     """t itself if the C ABI accepts its layout (unit inner stride, the others non-negative
     multiples of 8, 16-byte aligned data that reach to the end of the last row's last 16 bytes),
     else a copy with rows padded to a multiple of 8."""
+    if t.dtype is not torch.bfloat16:
+        raise B.TriAttnError(B.TRI_ATTN_ERR_DTYPE, f"a bias or its gradient must be torch.bfloat16, got {t.dtype}")
     n = t.shape[3]
     if t.data_ptr() % 16 == 0:
         if n % 8 == 0 and t.is_contiguous():
