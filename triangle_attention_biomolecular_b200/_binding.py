@@ -731,10 +731,11 @@ def tri_act8_unpack(codes, exps, kind: int, x, stream=None) -> None:
     _call((_lib or load()).tri_act8_unpack, a, "tri_act8_unpack", stream, x, codes, exps)
 
 
+_INT32 = torch.int32
+
+
 def _int32(t, name, dims) -> int:
-    if t is None:
-        return 0
-    if t.dtype is not torch.int32:
+    if t.dtype is not _INT32:
         raise TriAttnError(TRI_ATTN_ERR_DTYPE, f"{name} must be torch.int32, got {t.dtype}")
     if t.dim() != dims:
         raise TriAttnError(TRI_ATTN_ERR_SHAPE, f"{name} must have {dims} dims")
@@ -744,19 +745,20 @@ def _int32(t, name, dims) -> int:
 
 
 def _relpos_index(pos_q, pos_k, group_q, group_k, edges):
-    """(E, edges pointer, the positions' and groups' pointers, batch strides)."""
-    if (group_q is None) != (group_k is None):
-        raise TriAttnError(TRI_ATTN_ERR_NULL, "group_q and group_k are given together or not at all")
-    idx = (_int32(edges, "edges", 1), _int32(pos_q, "pos_q", 2), _int32(pos_k, "pos_k", 2),
-           _int32(group_q, "group_q", 2), _int32(group_k, "group_k", 2), pos_q.stride(0), pos_k.stride(0))
-    B = pos_q.shape[0]
+    """The edges' pointer, the positions' and groups' pointers, batch strides."""
+    ep, qp, kp = _int32(edges, "edges", 1), _int32(pos_q, "pos_q", 2), _int32(pos_k, "pos_k", 2)
+    qs, ks, B = pos_q.stride(0), pos_k.stride(0), pos_q.shape[0]
     if B != pos_k.shape[0]:
         raise TriAttnError(TRI_ATTN_ERR_SHAPE, "pos_q and pos_k must have one batch size")
-    if group_q is not None:
-        for g, p, n in ((group_q, pos_q, "group_q"), (group_k, pos_k, "group_k")):
-            if g.shape != p.shape or (B > 1 and g.stride(0) != p.stride(0)):
-                raise TriAttnError(TRI_ATTN_ERR_SHAPE, f"{n} must be laid out as its positions are")
-    return idx
+    if group_q is None and group_k is None:
+        return ep, qp, kp, 0, 0, qs, ks
+    if group_q is None or group_k is None:
+        raise TriAttnError(TRI_ATTN_ERR_NULL, "group_q and group_k are given together or not at all")
+    gqp, gkp = _int32(group_q, "group_q", 2), _int32(group_k, "group_k", 2)
+    if group_q.shape != pos_q.shape or group_k.shape != pos_k.shape or (
+            B > 1 and (group_q.stride(0) != qs or group_k.stride(0) != ks)):
+        raise TriAttnError(TRI_ATTN_ERR_SHAPE, "groups must be laid out as their positions are")
+    return ep, qp, kp, gqp, gkp, qs, ks
 
 
 def _relpos_bias(t, name, shape):

@@ -56,15 +56,13 @@ def _layout(t: torch.Tensor) -> torch.Tensor:
     else a copy with rows padded to a multiple of 8."""
     if t.dtype is not torch.bfloat16:
         raise B.TriAttnError(B.TRI_ATTN_ERR_DTYPE, f"a bias or its gradient must be torch.bfloat16, got {t.dtype}")
-    n = t.shape[3]
-    if t.data_ptr() % 16 == 0:
-        if n % 8 == 0 and t.is_contiguous():
+    b, h, q, n = t.shape
+    sb, sh, sq, sn = t.stride()
+    sb, sh, sq = sb if b > 1 else 0, sh if h > 1 else 0, sq if q > 1 else 0
+    if not (t.data_ptr() % 16 or sb % 8 or sh % 8 or sq % 8) and (sn == 1 or n == 1):
+        end = (b - 1) * sb + (h - 1) * sh + (q - 1) * sq + (n + 7) // 8 * 8
+        if n % 8 == 0 or 2 * (t.storage_offset() + end) <= t.untyped_storage().nbytes():
             return t
-        lead = [(m - 1) * s for m, s in zip(t.shape[:3], t.stride()[:3])]
-        if (n == 1 or t.stride(3) == 1) and all(s >= 0 and s % 8 == 0 for s in lead) and (
-                n % 8 == 0 or 2 * (t.storage_offset() + sum(lead) + (n + 7) // 8 * 8) <= t.untyped_storage().nbytes()):
-            if all(m == 1 or s % 8 == 0 for m, s in zip(t.shape[:3], t.stride()[:3])):
-                return t
     return _padded(t.shape, t).copy_(t)
 
 
@@ -72,16 +70,20 @@ def _padded(shape, like) -> torch.Tensor:
     *lead, n = shape
     if n % 8 == 0:
         return like.new_empty(shape, dtype=torch.bfloat16)
-    return like.new_empty((*lead, (n + 7) // 8 * 8), dtype=torch.bfloat16)[..., :n]
+    return like.new_empty((*lead, (n + 7) // 8 * 8), dtype=torch.bfloat16).narrow(-1, 0, n)
 
 
 def _index(pos_q, pos_k, group_q, group_k, like=None):
     """Positions and groups as int32 [B, N], one batch size (that of ``like`` where all are shared),
     groups laid out as the positions."""
+    if pos_q.dim() == 2 and pos_q.is_contiguous() and pos_k.dim() == 2 and pos_k.is_contiguous():
+        n = pos_q.shape[0]
+        if n == pos_k.shape[0] and (like is None or like.shape[0] == n) and (
+                group_q is None or group_k is None
+                or (group_q.shape == pos_q.shape and group_q.is_contiguous()
+                    and group_k.shape == pos_k.shape and group_k.is_contiguous())):
+            return pos_q, pos_k, group_q, group_k  # checked further where they are used
     ts = [pos_q, pos_k, group_q, group_k]
-    if all(t is None or (t.dim() == 2 and t.is_contiguous()) for t in ts) and pos_q.shape[0] == pos_k.shape[0] and (
-            like is None or like.shape[0] == pos_q.shape[0]):
-        return pos_q, pos_k, group_q, group_k  # checked where they are used
     for t in ts:
         if t is not None and (t.dtype != torch.int32 or not 1 <= t.dim() <= 2):
             raise B.TriAttnError(B.TRI_ATTN_ERR_DTYPE, f"positions and groups are int32 [N] or [B, N], got {t.dtype} {list(t.shape)}")
