@@ -4,8 +4,8 @@
 // attention reads.  A bucket serves all H heads, so a thread finds the buckets
 // of eight neighbouring keys once and then writes 16 bytes per head; the table
 // sits in shared memory.  Bound by the bytes of the bias: 2048 x 2048 x 16 heads
-// take 28 us, 4.8 TB/s of stores (20.4 us at the measured copy rate); 2 x 1031 x
-// 1031 x 12 heads, which the L2 cache holds, 19 us, bound by their instructions.
+// take 26 us, 5.2 TB/s of stores (20.4 us at the measured copy rate); 2 x 1031 x
+// 1031 x 12 heads, which the L2 cache holds, 17 us, bound by their instructions.
 //
 // Backward: dtable[k,h] = sum of dbias over the positions of bucket k, read
 // once.  No atomics: see tri_relpos_bwd_kernel.
@@ -168,7 +168,7 @@ __host__ constexpr size_t relpos_fwd_smem(int nb, int heads, bool base) {
 // many rows at a step as all threads together hold; neighbouring threads take
 // neighbouring chunks, so a warp's 16-byte stores lie side by side.  With the
 // table in FP32 throughout, and every chunk looked up key by key, the two sizes
-// above took 29 and 26 us.
+// above took 29 and 26 us; with warps split between the two ways, 28 and 19.
 template <bool BASE>
 __global__ void __launch_bounds__(kRelThreads, kRelFwdBlocks)
     tri_relpos_fwd_kernel(const __grid_constant__ RelposParams p) {
@@ -244,7 +244,11 @@ __global__ void __launch_bounds__(kRelThreads, kRelFwdBlocks)
             }
         } else {
             at[0] *= pitch;
+#pragma unroll
+            for (int x = 1; x < 8; ++x) at[x] = at[0];
         }
+        // the short way only where the whole warp can take it: a split warp would go both
+        one = __all_sync(__activemask(), one);
         __nv_bfloat16* out = p.bias + b * p.os[0] + h0 * p.os[1] + i * p.os[2] + j0;
         if constexpr (BASE) {
             const __nv_bfloat16* in = p.base + b * p.bs[0] + h0 * p.bs[1] + i * p.bs[2] + j0;
