@@ -105,13 +105,15 @@ void with_bool(bool v, F&& f) {
 
 // f(how the lanes share a row, whether a row takes a whole block)
 template <typename F>
-void with_mode(bool vec, int lanes, F&& f) {
+void with_mode(bool vec, int lanes, int C, F&& f) {
     if (lanes > 32)
         vec ? f(Int<tri::kVec>{}, std::true_type{}) : f(Int<tri::kBy32>{}, std::true_type{});
     else if (vec)
         f(Int<tri::kVec>{}, std::false_type{});
+    else if (lanes == tri::kBy4)
+        f(Int<tri::kBy4>{}, std::false_type{});
     else
-        lanes == tri::kBy4 ? f(Int<tri::kBy4>{}, std::false_type{}) : f(Int<tri::kBy32>{}, std::false_type{});
+        C <= 256 ? f(Int<tri::kBy32Half>{}, std::false_type{}) : f(Int<tri::kBy32>{}, std::false_type{});
 }
 
 // the ordered sum of partial sums, its launch overlapping the end of the kernel that writes them
@@ -154,7 +156,7 @@ tri_attn_status norm_fwd_impl(const tri_norm_fwd_args* a, bool restore, tri_attn
     const int per_sm = s.lanes > 32 ? 8 : tri::norm_fwd_blocks(vec, !restore && xe == 4);
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>((a->R + s.per_block - 1) / s.per_block, 148 * per_sm));
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    with_mode(vec, s.lanes, [&](auto m, auto wd) {
+    with_mode(vec, s.lanes, a->C, [&](auto m, auto wd) {
         constexpr int MODE = decltype(m)::value;
         constexpr bool WIDE = decltype(wd)::value;
         with_types(restore ? a->y_type : a->x_type, a->y_type, [&](auto tx, auto ty) {
@@ -209,7 +211,7 @@ tri_attn_status act8_impl(const tri_act8_args* a, bool pack, tri_attn_stream_t s
     const int per_sm = 2 * (vec ? tri::kAct8Blocks : tri::kAct8BlocksBy);
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>((items + per - 1) / per, 148 * per_sm));
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    with_mode(vec, p.lanes, [&](auto m, auto wd) {
+    with_mode(vec, p.lanes, C, [&](auto m, auto wd) {
         if constexpr (!decltype(wd)::value)  // pieces are no wider than a warp
             with_types(x_type, x_type, [&](auto tx, auto ty) {
                 using TX = decltype(tx);
@@ -364,7 +366,7 @@ tri_attn_status tri_norm_bwd(const tri_norm_bwd_args* a, tri_attn_stream_t strea
     p.db = a->db;
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     if (blocks) {
-        with_mode(vec, s.lanes, [&](auto m, auto wd) {
+        with_mode(vec, s.lanes, f.C, [&](auto m, auto wd) {
             constexpr int MODE = decltype(m)::value;
             constexpr bool WIDE = decltype(wd)::value;
             with_types(f.x_type, f.y_type, [&](auto tx, auto ty) {

@@ -59,8 +59,13 @@ struct NormParams {
 // moved in aligned vectors.  Rows that cannot be moved so are walked element by
 // element, neighbouring lanes on neighbouring channels, with a stride that the
 // compiler knows: by 4 lanes (up to 64 channels: 8 rows per warp) or by whole
-// warps, 512 channels each, where lane l has l, l + 32, l + 64, ...
-enum : int { kVec = 0, kBy4 = 4, kBy32 = 32 };
+// warps, 512 channels each, where lane l has l, l + 32, l + 64, ...; rows of up to
+// 256 channels have kBy32Half, eight channels per lane in place of sixteen, since
+// those that a lane does not have would cost their instructions all the same.
+enum : int { kVec = 0, kBy4 = 4, kBy32 = 32, kBy32Half = 33 };
+// channels per lane, and the lanes' stride where they are not neighbours
+__host__ __device__ constexpr int norm_n(int mode) { return mode == kBy32Half ? 8 : 16; }
+__host__ __device__ constexpr int norm_stride(int mode) { return mode == kBy32Half ? 32 : mode; }
 template <int MODE>
 __device__ __forceinline__ int norm_col(int g, int k) {
     if constexpr (MODE == kVec) return g * 16 + k;
@@ -92,7 +97,7 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float v) {
 // (past C, or of a row that does not exist) read as 0.
 template <typename T, int MODE>
 struct NormRow {
-    uint32_t w[MODE == kVec && sizeof(T) == 2 ? 8 : 16];
+    uint32_t w[MODE == kVec && sizeof(T) == 2 ? 8 : norm_n(MODE)];
     __device__ __forceinline__ void load(const void* base, int64_t off, bool ok, int g, int G, int C) {
         const T* row = static_cast<const T*>(base) + off;
         if constexpr (MODE == kVec) {
@@ -105,7 +110,7 @@ struct NormRow {
             }
         } else {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
+            for (int k = 0; k < norm_n(MODE); ++k) {
                 const int c = norm_col<MODE>(g, k);
                 w[k] = 0u;
                 if (ok && c < C) {
@@ -117,9 +122,9 @@ struct NormRow {
             }
         }
     }
-    __device__ __forceinline__ void values(float2 (&v)[8]) const {
+    __device__ __forceinline__ void values(float2 (&v)[norm_n(MODE) / 2]) const {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
+        for (int k = 0; k < norm_n(MODE) / 2; ++k) {
             if constexpr (MODE == kVec && sizeof(T) == 2)
                 v[k] = bf16x2_to_f2(w[k]);
             else
@@ -129,7 +134,8 @@ struct NormRow {
 };
 
 template <typename T, int MODE>
-__device__ __forceinline__ void store16(void* base, int64_t off, bool ok, int g, int G, int C, const float2 (&v)[8]) {
+__device__ __forceinline__ void store16(void* base, int64_t off, bool ok, int g, int G, int C,
+                                        const float2 (&v)[norm_n(MODE) / 2]) {
     T* row = static_cast<T*>(base) + off;
     if constexpr (MODE == kVec) {
         if (ok && g * 16 < C) {
@@ -150,7 +156,7 @@ __device__ __forceinline__ void store16(void* base, int64_t off, bool ok, int g,
         }
     } else {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
+        for (int k = 0; k < norm_n(MODE); ++k) {
             const int c = norm_col<MODE>(g, k);
             if (ok && c < C) row[c] = from_f32<T>(k & 1 ? v[k / 2].y : v[k / 2].x);
         }
@@ -167,17 +173,17 @@ __device__ __forceinline__ float norm_param(const void* p, int is_bf16, float ab
 }
 template <int MODE, bool WIDE>
 struct NormParam {
-    float2 own[WIDE ? 8 : 1];
+    float2 own[WIDE ? norm_n(MODE) / 2 : 1];
     const float* sh;
     __device__ __forceinline__ void init(const void* p, int is_bf16, float absent, int g, int G, int C, float* shared) {
         sh = shared;
         if constexpr (WIDE) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
+            for (int k = 0; k < norm_n(MODE) / 2; ++k)
                 own[k] = make_float2(norm_param(p, is_bf16, absent, norm_col<MODE>(g, 2 * k), C),
                                      norm_param(p, is_bf16, absent, norm_col<MODE>(g, 2 * k + 1), C));
         } else {
-            for (int x = threadIdx.x; x < 16 * G; x += blockDim.x) {
+            for (int x = threadIdx.x; x < norm_n(MODE) * G; x += blockDim.x) {
                 const int lane = (x >> 2) & (G - 1), q = (x >> 2) / G;
                 shared[x] = norm_param(p, is_bf16, absent, MODE == kVec ? lane * 16 + q * 4 + (x & 3) : x, C);
             }
@@ -194,8 +200,9 @@ struct NormParam {
             b = make_float2(v.z, v.w);
         } else {
             const float* s = sh + norm_col<MODE>(g, 4 * q);
-            a = make_float2(s[0], s[MODE]);
-            b = make_float2(s[2 * MODE], s[3 * MODE]);
+            constexpr int kStride = norm_stride(MODE);
+            a = make_float2(s[0], s[kStride]);
+            b = make_float2(s[2 * kStride], s[3 * kStride]);
         }
     }
 };
@@ -290,8 +297,8 @@ __device__ __forceinline__ float absmax3(float a, float b, float c) {
 // this lane's sixteen channels, from channel c0 of their row on, into its 8-bit form; every lane of
 // the warp calls it
 template <int ACT, int MODE>
-__device__ __forceinline__ void act8_emit(const NormParams& p, int64_t row, bool ok, int g, int G, const float2 (&u)[8],
-                                          int c0 = 0) {
+__device__ __forceinline__ void act8_emit(const NormParams& p, int64_t row, bool ok, int g, int G,
+                                          const float2 (&u)[norm_n(MODE) / 2], int c0 = 0) {
     const int C = p.C - c0;
     uint8_t* codes = p.codes + row * p.cs + c0;
     uint8_t* exps = p.exps + row * p.es + c0 / 32;
@@ -315,15 +322,16 @@ __device__ __forceinline__ void act8_emit(const NormParams& p, int64_t row, bool
             if ((g & 1) == 0) exps[g >> 1] = static_cast<uint8_t>(eb);
         }
     } else {
-        float v[16];
-        uint32_t a[16];
+        constexpr int N = norm_n(MODE);
+        float v[N];
+        uint32_t a[N];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) v[k] = k & 1 ? u[k / 2].y : u[k / 2].x;
+        for (int k = 0; k < N; ++k) v[k] = k & 1 ? u[k / 2].y : u[k / 2].x;
 #pragma unroll
-        for (int k = 0; k < 16; ++k) a[k] = __float_as_uint(v[k]) & 0x7FFFFFFFu;
-        if constexpr (MODE == kBy32) {
+        for (int k = 0; k < N; ++k) a[k] = __float_as_uint(v[k]) & 0x7FFFFFFFu;
+        if constexpr (MODE != kBy4) {
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
+            for (int k = 0; k < N; ++k)
                 if (32 * k < C) a[k] = __reduce_max_sync(0xFFFFFFFFu, a[k]);
         } else {  // a block is eight k of four lanes
 #pragma unroll
@@ -337,7 +345,7 @@ __device__ __forceinline__ void act8_emit(const NormParams& p, int64_t row, bool
             }
         }
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
+        for (int k = 0; k < N; ++k) {
             const int c = norm_col<MODE>(g, k);
             if (ok && c < C) {
                 const uint32_t eb = act8_exp<ACT>(a[k]);
@@ -352,7 +360,7 @@ __device__ __forceinline__ void act8_emit(const NormParams& p, int64_t row, bool
 // sixteen channels of the 8-bit form of a row, as loaded
 template <int ACT, int MODE>
 struct NormRow8 {
-    uint32_t w[MODE == kVec ? 4 : 16], e[MODE == kVec ? 1 : 16];
+    uint32_t w[MODE == kVec ? 4 : norm_n(MODE)], e[MODE == kVec ? 1 : norm_n(MODE)];
     __device__ __forceinline__ void load(const NormParams& p, int64_t row, bool ok, int g, int G, int c0 = 0) {
         const int C = p.C - c0;
         const uint8_t* codes = p.codes + row * p.cs + c0;
@@ -369,7 +377,7 @@ struct NormRow8 {
             }
         } else {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
+            for (int k = 0; k < norm_n(MODE); ++k) {
                 const int c = norm_col<MODE>(g, k);
                 w[k] = e[k] = 0u;
                 if (ok && c < C) {
@@ -379,14 +387,14 @@ struct NormRow8 {
             }
         }
     }
-    __device__ __forceinline__ void values(float2 (&v)[8]) const {
+    __device__ __forceinline__ void values(float2 (&v)[norm_n(MODE) / 2]) const {
         if constexpr (MODE == kVec) {
             const float s = act8_scale(e[0]);
 #pragma unroll
             for (int q = 0; q < 4; ++q) act8_value4<ACT>(w[q], s, v + 2 * q);
         } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
+            for (int k = 0; k < norm_n(MODE) / 2; ++k)
                 v[k] = make_float2(act8_value<ACT>(w[2 * k]) * act8_scale(e[2 * k]),
                                    act8_value<ACT>(w[2 * k + 1]) * act8_scale(e[2 * k + 1]));
         }
@@ -449,7 +457,8 @@ __global__ void __launch_bounds__(WIDE ? 32 * kNormMaxWarps : kNormThreads,
     __shared__ float2 red[2][kNormMaxWarps];
     __shared__ __align__(16) float sh_w[WIDE ? 4 : 512], sh_b[WIDE ? 4 : 512];
     const bool dead = device_error_pending();
-    const int G = MODE == kVec || WIDE ? p.lanes : MODE;
+    constexpr int N = norm_n(MODE), N2 = N / 2;  // channels and pairs of them per lane
+    const int G = MODE == kVec || WIDE ? p.lanes : norm_stride(MODE);
     const int g = WIDE ? static_cast<int>(threadIdx.x) : static_cast<int>(threadIdx.x) & (G - 1);
     const int per_block = WIDE ? 1 : kNormThreads / G, sub = WIDE ? 0 : threadIdx.x / G;
     int turn = 0;
@@ -479,25 +488,25 @@ __global__ void __launch_bounds__(WIDE ? 32 * kNormMaxWarps : kNormThreads,
     for (; base < p.R; base += step) {
         const int64_t row = base + sub;
         const bool st = row < p.R && !dead;
-        float2 v[8];
+        float2 v[N2];
         if constexpr (RESTORE) {
             if constexpr (!kAhead) load(row);
             next8.values(v);
             const float m = mean, r = rstd;
             if constexpr (kAhead) load(row + step);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = fmul2(fadd2(v[k], splat(-m)), splat(r));
+            for (int k = 0; k < N2; ++k) v[k] = fmul2(fadd2(v[k], splat(-m)), splat(r));
         } else {
             next.values(v);
             load(row + step);
             if constexpr (ACT != ACT_NONE) act8_emit<ACT, MODE>(p, row, st, g, G, v);
             float2 s = fadd2(v[0], v[1]);
 #pragma unroll
-            for (int k = 2; k < 8; ++k) s = fadd2(s, v[k]);
+            for (int k = 2; k < N2; ++k) s = fadd2(s, v[k]);
             mean = row_sum<WIDE>(s.x + s.y, G, red, turn) * p.inv_c;
             s = splat(0.f);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < N2; ++k) {
                 v[k] = fadd2(v[k], splat(-mean));
                 if constexpr (MODE != kVec) {
                     if (norm_col<MODE>(g, 2 * k) >= p.C) v[k].x = 0.f;
@@ -512,10 +521,10 @@ __global__ void __launch_bounds__(WIDE ? 32 * kNormMaxWarps : kNormThreads,
                 p.stats[p.R + row] = rstd;
             }
 #pragma unroll
-            for (int k = 0; k < 8; ++k) v[k] = fmul2(v[k], splat(rstd));
+            for (int k = 0; k < N2; ++k) v[k] = fmul2(v[k], splat(rstd));
         }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < N / 4; ++q) {
             float2 wa, wb, ba, bb;
             w.get4(q, g, G, wa, wb);
             b.get4(q, g, G, ba, bb);
@@ -547,15 +556,16 @@ __global__ void __launch_bounds__(WIDE ? 32 * kNormMaxWarps : kNormThreads, WIDE
     __shared__ __align__(16) float sh_w[WIDE ? 4 : 512];
     grid_dependents_start();
     const bool dead = device_error_pending();
-    const int G = MODE == kVec || WIDE ? p.lanes : MODE;
+    constexpr int N = norm_n(MODE), N2 = N / 2;  // channels and pairs of them per lane
+    const int G = MODE == kVec || WIDE ? p.lanes : norm_stride(MODE);
     const int g = WIDE ? static_cast<int>(threadIdx.x) : static_cast<int>(threadIdx.x) & (G - 1);
     const int per_block = WIDE ? 1 : kNormThreads / G, sub = WIDE ? 0 : threadIdx.x / G;
     int turn = 0;
     NormParam<MODE, WIDE> w;
     w.init(p.w, p.w_bf16, 1.f, g, G, p.C, sh_w);
-    float2 dw[8], db[8];
+    float2 dw[N2], db[N2];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) dw[k] = db[k] = splat(0.f);
+    for (int k = 0; k < N2; ++k) dw[k] = db[k] = splat(0.f);
     NormRow<TX, MODE> nx;
     NormRow8<ACT, MODE> nx8;
     NormRow<TY, MODE> nd;
@@ -578,7 +588,7 @@ __global__ void __launch_bounds__(WIDE ? 32 * kNormMaxWarps : kNormThreads, WIDE
     for (; base < p.R; base += step) {
         const int64_t row = base + sub;
         const bool st = row < p.R && !dead;
-        float2 h[8], d[8];
+        float2 h[N2], d[N2];
         if constexpr (!kAhead) load(row);
         if constexpr (ACT != ACT_NONE)
             nx8.values(h);
@@ -589,7 +599,7 @@ __global__ void __launch_bounds__(WIDE ? 32 * kNormMaxWarps : kNormThreads, WIDE
         if constexpr (kAhead) load(row + step);
         float2 sa = splat(0.f), sb = splat(0.f);
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < N / 4; ++q) {
             float2 ww[2];
             w.get4(q, g, G, ww[0], ww[1]);
 #pragma unroll
@@ -608,7 +618,7 @@ __global__ void __launch_bounds__(WIDE ? 32 * kNormMaxWarps : kNormThreads, WIDE
             const float2 c1 = splat(s.x * p.inv_c), c2 = splat(-s.y * p.inv_c);
             const float2 n1 = make_float2(-c1.x, -c1.y);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) d[k] = fmul2(fadd2(d[k], ffma2(h[k], c2, n1)), splat(r));
+            for (int k = 0; k < N2; ++k) d[k] = fmul2(fadd2(d[k], ffma2(h[k], c2, n1)), splat(r));
             store16<TX, MODE>(p.dx, row * p.dxs, st, g, G, p.C, d);
         }
     }
@@ -617,7 +627,7 @@ __global__ void __launch_bounds__(WIDE ? 32 * kNormMaxWarps : kNormThreads, WIDE
     float* out_b = gridDim.x == 1 ? p.db : out_w + p.C;
     if constexpr (WIDE) {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
+        for (int k = 0; k < N; ++k) {
             const int c = norm_col<MODE>(g, k);
             if (c < p.C && !dead) {
                 out_w[c] = k & 1 ? dw[k / 2].y : dw[k / 2].x;
@@ -628,7 +638,7 @@ __global__ void __launch_bounds__(WIDE ? 32 * kNormMaxWarps : kNormThreads, WIDE
         // the rows of a warp, then the warps of the block
         for (int m = G; m < 32; m <<= 1) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < N2; ++k) {
                 dw[k].x += __shfl_xor_sync(0xFFFFFFFFu, dw[k].x, m);
                 dw[k].y += __shfl_xor_sync(0xFFFFFFFFu, dw[k].y, m);
                 db[k].x += __shfl_xor_sync(0xFFFFFFFFu, db[k].x, m);
@@ -638,7 +648,7 @@ __global__ void __launch_bounds__(WIDE ? 32 * kNormMaxWarps : kNormThreads, WIDE
         const int warp = threadIdx.x >> 5;
         if ((threadIdx.x & 31) < G) {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
+            for (int k = 0; k < N; ++k) {
                 sums[warp][0][norm_col<MODE>(g, k)] = k & 1 ? dw[k / 2].y : dw[k / 2].x;
                 sums[warp][1][norm_col<MODE>(g, k)] = k & 1 ? db[k / 2].y : db[k / 2].x;
             }
@@ -695,7 +705,7 @@ template <typename TX, int ACT, int MODE, bool PACK>
 __global__ void __launch_bounds__(kNormThreads, MODE == kVec ? kAct8Blocks : kAct8BlocksBy)
     tri_act8_kernel(const __grid_constant__ NormParams p) {
     const bool dead = device_error_pending();
-    const int G = MODE == kVec ? p.lanes : MODE;
+    const int G = MODE == kVec ? p.lanes : norm_stride(MODE);
     const int g = static_cast<int>(threadIdx.x) & (G - 1), per_block = kNormThreads / G;
     const int pieces = (p.C + 511) / 512;
     const int64_t items = p.R * pieces, step = static_cast<int64_t>(gridDim.x) * per_block;
@@ -709,7 +719,7 @@ __global__ void __launch_bounds__(kNormThreads, MODE == kVec ? kAct8Blocks : kAc
             c0 = static_cast<int>(item - row * pieces) * 512;
         }
         // a piece ends where the next one begins: the lanes cover no more than 512 channels
-        float2 v[8];
+        float2 v[norm_n(MODE) / 2];
         if constexpr (PACK) {
             NormRow<TX, MODE> r;
             r.load(p.x, row * p.xs + c0, ok, g, G, p.C - c0);
