@@ -35,17 +35,22 @@ bool vec_rows(const void* p, int64_t stride, int64_t elem) { return aligned_to(p
 bool vec_act8(const tri_act8& a) { return aligned_to(a.codes, 16) && a.codes_stride % 16 == 0; }
 
 struct NormShape {
-    int lanes, threads;
+    int mode, lanes, threads;
     int64_t per_block;
 };
 NormShape norm_shape(int C, bool vec) {
     const int units = (C + 15) / 16;
     NormShape s{};
     s.threads = tri::kNormThreads;
+    s.mode = vec                ? tri::kVec
+             : units <= 4       ? tri::kBy4
+             : C <= 128         ? tri::kBy32Quarter
+             : C <= 256         ? tri::kBy32Half
+                                : tri::kBy32;
     if (units > 32)
         s.lanes = s.threads = (units + 31) / 32 * 32;
     else if (!vec)
-        s.lanes = units <= 4 ? tri::kBy4 : tri::kBy32;
+        s.lanes = tri::norm_stride(s.mode);
     else
         for (s.lanes = 1; s.lanes < units;) s.lanes *= 2;
     s.per_block = s.threads / s.lanes;
@@ -58,7 +63,7 @@ int64_t norm_bwd_blocks(int64_t R, int C, bool vec) {
     // few rows: one block goes through them, and the launch that adds up partial sums is saved
     // (64 rows of 128: 17.5 us of host time and 4.4 us of the device's, against 19.7 and 6.4)
     if (R > 0 && R <= 4 * s.per_block) return 1;
-    return std::min<int64_t>((R + s.per_block - 1) / s.per_block, 148 * (s.lanes > 32 ? 4 : tri::kNormBwdBlocks));
+    return std::min<int64_t>((R + s.per_block - 1) / s.per_block, 148 * (s.lanes > 32 ? 4 : tri::norm_bwd_per_sm(s.mode)));
 }
 
 void norm_params(NormParams& p, const tri_norm_fwd_args& a, const NormShape& s) {
@@ -105,15 +110,17 @@ void with_bool(bool v, F&& f) {
 
 // f(how the lanes share a row, whether a row takes a whole block)
 template <typename F>
-void with_mode(bool vec, int lanes, int C, F&& f) {
-    if (lanes > 32)
-        vec ? f(Int<tri::kVec>{}, std::true_type{}) : f(Int<tri::kBy32>{}, std::true_type{});
-    else if (vec)
+void with_mode(const NormShape& s, F&& f) {
+    if (s.lanes > 32)
+        s.mode == tri::kVec ? f(Int<tri::kVec>{}, std::true_type{}) : f(Int<tri::kBy32>{}, std::true_type{});
+    else if (s.mode == tri::kVec)
         f(Int<tri::kVec>{}, std::false_type{});
-    else if (lanes == tri::kBy4)
+    else if (s.mode == tri::kBy4)
         f(Int<tri::kBy4>{}, std::false_type{});
+    else if (s.mode == tri::kBy32Quarter)
+        f(Int<tri::kBy32Quarter>{}, std::false_type{});
     else
-        C <= 256 ? f(Int<tri::kBy32Half>{}, std::false_type{}) : f(Int<tri::kBy32>{}, std::false_type{});
+        s.mode == tri::kBy32Half ? f(Int<tri::kBy32Half>{}, std::false_type{}) : f(Int<tri::kBy32>{}, std::false_type{});
 }
 
 // the ordered sum of partial sums, its launch overlapping the end of the kernel that writes them
@@ -153,10 +160,10 @@ tri_attn_status norm_fwd_impl(const tri_norm_fwd_args* a, bool restore, tri_attn
     const NormShape s = norm_shape(a->C, vec);
     NormParams p{};
     norm_params(p, *a, s);
-    const int per_sm = s.lanes > 32 ? 8 : tri::norm_fwd_blocks(vec, !restore && xe == 4);
+    const int per_sm = s.lanes > 32 ? 8 : tri::norm_fwd_blocks(s.mode, !restore && xe == 4);
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>((a->R + s.per_block - 1) / s.per_block, 148 * per_sm));
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    with_mode(vec, s.lanes, a->C, [&](auto m, auto wd) {
+    with_mode(s, [&](auto m, auto wd) {
         constexpr int MODE = decltype(m)::value;
         constexpr bool WIDE = decltype(wd)::value;
         with_types(restore ? a->y_type : a->x_type, a->y_type, [&](auto tx, auto ty) {
@@ -198,7 +205,8 @@ tri_attn_status act8_impl(const tri_act8_args* a, bool pack, tri_attn_stream_t s
     NormParams p{};
     p.R = R;
     p.C = C;
-    p.lanes = norm_shape(std::min(C, 512), vec).lanes;
+    const NormShape s = norm_shape(std::min(C, 512), vec);
+    p.lanes = s.lanes;
     p.x = x;
     p.xs = xs;
     p.y = x;
@@ -208,10 +216,10 @@ tri_attn_status act8_impl(const tri_act8_args* a, bool pack, tri_attn_stream_t s
     p.exps = static_cast<uint8_t*>(act.exps);
     p.es = act.exps_stride;
     const int64_t per = tri::kNormThreads / p.lanes, items = R * pieces;
-    const int per_sm = 2 * (vec ? tri::kAct8Blocks : tri::kAct8BlocksBy);
+    const int per_sm = 2 * tri::act8_blocks(s.mode);
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>((items + per - 1) / per, 148 * per_sm));
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    with_mode(vec, p.lanes, C, [&](auto m, auto wd) {
+    with_mode(s, [&](auto m, auto wd) {
         if constexpr (!decltype(wd)::value)  // pieces are no wider than a warp
             with_types(x_type, x_type, [&](auto tx, auto ty) {
                 using TX = decltype(tx);
@@ -366,7 +374,7 @@ tri_attn_status tri_norm_bwd(const tri_norm_bwd_args* a, tri_attn_stream_t strea
     p.db = a->db;
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     if (blocks) {
-        with_mode(vec, s.lanes, f.C, [&](auto m, auto wd) {
+        with_mode(s, [&](auto m, auto wd) {
             constexpr int MODE = decltype(m)::value;
             constexpr bool WIDE = decltype(wd)::value;
             with_types(f.x_type, f.y_type, [&](auto tx, auto ty) {

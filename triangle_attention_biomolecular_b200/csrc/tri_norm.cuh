@@ -60,12 +60,17 @@ struct NormParams {
 // element, neighbouring lanes on neighbouring channels, with a stride that the
 // compiler knows: by 4 lanes (up to 64 channels: 8 rows per warp) or by whole
 // warps, 512 channels each, where lane l has l, l + 32, l + 64, ...; rows of up to
-// 256 channels have kBy32Half, eight channels per lane in place of sixteen, since
-// those that a lane does not have would cost their instructions all the same.
-enum : int { kVec = 0, kBy4 = 4, kBy32 = 32, kBy32Half = 33 };
+// 256 (128) channels have kBy32Half (kBy32Quarter), eight (four) channels per lane
+// in place of sixteen, since those that a lane does not have would cost their
+// instructions and registers all the same: 200000 rows of 100 BF16 channels take
+// 36 us forward and 47 us backward in place of 74 and 208, 209 FP32 channels 62 and
+// 86 in place of 78 and 105.
+enum : int { kVec = 0, kBy4 = 4, kBy32 = 32, kBy32Half = 33, kBy32Quarter = 34 };
 // channels per lane, and the lanes' stride where they are not neighbours
-__host__ __device__ constexpr int norm_n(int mode) { return mode == kBy32Half ? 8 : 16; }
-__host__ __device__ constexpr int norm_stride(int mode) { return mode == kBy32Half ? 32 : mode; }
+__host__ __device__ constexpr int norm_n(int mode) {
+    return mode == kBy32Quarter ? 4 : mode == kBy32Half ? 8 : 16;
+}
+__host__ __device__ constexpr int norm_stride(int mode) { return mode > kBy32 ? 32 : mode; }
 template <int MODE>
 __device__ __forceinline__ int norm_col(int g, int k) {
     if constexpr (MODE == kVec) return g * 16 + k;
@@ -412,8 +417,10 @@ constexpr int kNormThreads = 256;   // rows of up to 512 channels: 256 / G of th
 constexpr int kNormMaxWarps = 16;   // rows of up to 8192 channels: one block, a warp per 512
 // Blocks per SM.  A row on its way takes eight registers in BF16 and sixteen in FP32 or element by
 // element, so those get the registers of a block less.
-constexpr int kNormBwdBlocks = 2;
-__host__ __device__ constexpr int norm_fwd_blocks(bool vec, bool f32) { return vec && !f32 ? 4 : 3; }
+__host__ __device__ constexpr int norm_fwd_blocks(int mode, bool f32) {
+    return mode == kBy32Quarter ? 5 : mode == kBy32Half || (mode == kVec && !f32) ? 4 : 3;
+}
+__host__ __device__ constexpr int norm_bwd_per_sm(int mode) { return mode == kBy32Quarter ? 4 : mode == kBy32Half ? 3 : 2; }
 
 // Sums over the G lanes of this lane's row, the same bits in every lane.  Rows
 // of more than one warp meet in shared memory; `turn` alternates between two
@@ -452,7 +459,7 @@ __device__ __forceinline__ float2 splat(float v) { return make_float2(v, v); }
 // ---------------------------------------------------------------------------
 template <typename TX, typename TY, int ACT, int MODE, bool RESTORE, bool WIDE>
 __global__ void __launch_bounds__(WIDE ? 32 * kNormMaxWarps : kNormThreads,
-                                  WIDE ? 1 : norm_fwd_blocks(MODE == kVec, sizeof(TX) == 4 && !RESTORE))
+                                  WIDE ? 1 : norm_fwd_blocks(MODE, sizeof(TX) == 4 && !RESTORE))
     tri_norm_fwd_kernel(const __grid_constant__ NormParams p) {
     __shared__ float2 red[2][kNormMaxWarps];
     __shared__ __align__(16) float sh_w[WIDE ? 4 : 512], sh_b[WIDE ? 4 : 512];
@@ -549,7 +556,7 @@ __device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepco
 // added in block order by tri_ordered_sum_kernel.  The number of blocks is a
 // function of the sizes alone, and so is every order of additions.
 template <typename TX, typename TY, int ACT, int MODE, bool WIDE>
-__global__ void __launch_bounds__(WIDE ? 32 * kNormMaxWarps : kNormThreads, WIDE ? 1 : kNormBwdBlocks)
+__global__ void __launch_bounds__(WIDE ? 32 * kNormMaxWarps : kNormThreads, WIDE ? 1 : norm_bwd_per_sm(MODE))
     tri_norm_bwd_kernel(const __grid_constant__ NormParams p) {
     __shared__ float2 red[2][kNormMaxWarps];
     __shared__ __align__(16) float sums[WIDE ? 1 : kNormThreads / 32][2][WIDE ? 1 : 512];
@@ -698,11 +705,11 @@ __global__ void __launch_bounds__(1024) tri_ordered_sum_kernel(const float* __re
 // into pieces of 512, a warp each.  What hides the latency here is many warps: with
 // a row loaded ahead, for which two blocks per SM less fit, 640 x 640 rows of 128
 // BF16 channels packed in 36 us instead of 31 (5.2 TB/s; unpacking 27 us, 5.9 TB/s).
-// Element by element, 20011 rows of 209 FP32 channels take 13 and 8 us, bound by
-// latency: each warp has two rows.
-constexpr int kAct8Blocks = 6, kAct8BlocksBy = 4;  // per SM
+// Element by element, 20011 rows of 209 FP32 channels take 10.5 and 7.5 us, bound
+// by their instructions.
+__host__ __device__ constexpr int act8_blocks(int mode) { return mode == kVec || mode == kBy32Quarter ? 6 : 4; }  // per SM
 template <typename TX, int ACT, int MODE, bool PACK>
-__global__ void __launch_bounds__(kNormThreads, MODE == kVec ? kAct8Blocks : kAct8BlocksBy)
+__global__ void __launch_bounds__(kNormThreads, act8_blocks(MODE))
     tri_act8_kernel(const __grid_constant__ NormParams p) {
     const bool dead = device_error_pending();
     const int G = MODE == kVec ? p.lanes : norm_stride(MODE);
