@@ -58,13 +58,14 @@ struct NormParams {
 // How the lanes of a row share its channels.  kVec: lane g has 16 g .. 16 g + 15,
 // moved in aligned vectors.  Rows that cannot be moved so are walked element by
 // element, neighbouring lanes on neighbouring channels, with a stride that the
-// compiler knows: by 4 lanes (up to 64 channels: 8 rows per warp) or by whole
-// warps, 512 channels each, where lane l has l, l + 32, l + 64, ...; rows of up to
-// 256 (128) channels have kBy32Half (kBy32Quarter), eight (four) channels per lane
-// in place of sixteen, since those that a lane does not have would cost their
-// instructions and registers all the same: 200000 rows of 100 BF16 channels take
-// 36 us forward and 47 us backward in place of 74 and 208, 209 FP32 channels 62 and
-// 86 in place of 78 and 105.
+// compiler knows: by 4 lanes (up to 64 channels: 8 rows per warp; 400000 rows of 50
+// BF16 channels take 35 us forward, 70 with a warp per row) or by whole warps, 512
+// channels each, where lane l has l, l + 32, l + 64, ...  Rows of up to 256 (128)
+// channels have kBy32Half (kBy32Quarter), eight (four) channels per lane in place of
+// sixteen, since those that a lane does not have would cost their instructions and
+// registers all the same: 200000 rows of 100 BF16 channels take 36 us forward and
+// 47 us backward in place of 74 and 208, 209 FP32 channels 62 and 86 in place of 78
+// and 105.
 enum : int { kVec = 0, kBy4 = 4, kBy32 = 32, kBy32Half = 33, kBy32Quarter = 34 };
 // channels per lane, and the lanes' stride where they are not neighbours
 __host__ __device__ constexpr int norm_n(int mode) {
