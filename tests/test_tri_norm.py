@@ -231,7 +231,7 @@ CASES = [  # R, C, x, y, weight (None: no affine), padding of the rows
     (300, 128, BF, F32, None, 16), (300, 128, F32, F32, F32, 1), (77, 1, BF, BF, F32, 0), (77, 2, F32, F32, F32, 0),
     (129, 16, BF, BF, F32, 0), (129, 17, F32, BF, BF, 0), (65, 31, BF, BF, F32, 0), (65, 32, F32, F32, F32, 0),
     (65, 33, BF, F32, F32, 0), (64, 48, BF, BF, None, 0), (64, 112, F32, F32, F32, 0), (50, 255, BF, BF, F32, 0),
-    (50, 387, F32, F32, F32, 0), (50, 384, BF, BF, F32, 0), (33, 512, BF, BF, F32, 0), (33, 513, BF, BF, F32, 0),
+    (70, 100, BF, BF, F32, 0), (1300, 67, F32, BF, BF, 0), (900, 200, F32, F32, F32, 0), (50, 387, F32, F32, F32, 0), (50, 384, BF, BF, F32, 0), (33, 512, BF, BF, F32, 0), (33, 513, BF, BF, F32, 0),
     (33, 528, F32, F32, BF, 0), (700, 1024, BF, BF, F32, 0), (20, 1025, F32, BF, F32, 0), (9, 8192, BF, BF, F32, 0),
     (9, 8191, F32, F32, F32, 3), (3000, 640, BF, BF, F32, 0),
 ]

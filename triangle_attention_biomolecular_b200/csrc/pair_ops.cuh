@@ -38,13 +38,14 @@ struct NormShape {
     int mode, lanes, threads;
     int64_t per_block;
 };
-NormShape norm_shape(int C, bool vec) {
+// alone: the 8-bit activation by itself, whose rows of 65 to 128 channels go by 8 lanes (see kBy8)
+NormShape norm_shape(int C, bool vec, bool alone = false) {
     const int units = (C + 15) / 16;
     NormShape s{};
     s.threads = tri::kNormThreads;
     s.mode = vec                ? tri::kVec
              : units <= 4       ? tri::kBy4
-             : C <= 128         ? tri::kBy32Quarter
+             : C <= 128         ? (alone ? tri::kBy8 : tri::kBy32Quarter)
              : C <= 256         ? tri::kBy32Half
                                 : tri::kBy32;
     if (units > 32)
@@ -109,16 +110,17 @@ void with_bool(bool v, F&& f) {
 }
 
 // f(how the lanes share a row, whether a row takes a whole block)
-template <typename F>
+template <bool ALONE, typename F>
 void with_mode(const NormShape& s, F&& f) {
+    constexpr int kTo128 = ALONE ? tri::kBy8 : tri::kBy32Quarter;
     if (s.lanes > 32)
         s.mode == tri::kVec ? f(Int<tri::kVec>{}, std::true_type{}) : f(Int<tri::kBy32>{}, std::true_type{});
     else if (s.mode == tri::kVec)
         f(Int<tri::kVec>{}, std::false_type{});
     else if (s.mode == tri::kBy4)
         f(Int<tri::kBy4>{}, std::false_type{});
-    else if (s.mode == tri::kBy32Quarter)
-        f(Int<tri::kBy32Quarter>{}, std::false_type{});
+    else if (s.mode == kTo128)
+        f(Int<kTo128>{}, std::false_type{});
     else
         s.mode == tri::kBy32Half ? f(Int<tri::kBy32Half>{}, std::false_type{}) : f(Int<tri::kBy32>{}, std::false_type{});
 }
@@ -163,7 +165,7 @@ tri_attn_status norm_fwd_impl(const tri_norm_fwd_args* a, bool restore, tri_attn
     const int per_sm = s.lanes > 32 ? 8 : tri::norm_fwd_blocks(s.mode, !restore && xe == 4);
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>((a->R + s.per_block - 1) / s.per_block, 148 * per_sm));
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    with_mode(s, [&](auto m, auto wd) {
+    with_mode<false>(s, [&](auto m, auto wd) {
         constexpr int MODE = decltype(m)::value;
         constexpr bool WIDE = decltype(wd)::value;
         with_types(restore ? a->y_type : a->x_type, a->y_type, [&](auto tx, auto ty) {
@@ -205,7 +207,7 @@ tri_attn_status act8_impl(const tri_act8_args* a, bool pack, tri_attn_stream_t s
     NormParams p{};
     p.R = R;
     p.C = C;
-    const NormShape s = norm_shape(std::min(C, 512), vec);
+    const NormShape s = norm_shape(std::min(C, 512), vec, true);
     p.lanes = s.lanes;
     p.x = x;
     p.xs = xs;
@@ -219,7 +221,7 @@ tri_attn_status act8_impl(const tri_act8_args* a, bool pack, tri_attn_stream_t s
     const int per_sm = 2 * tri::act8_blocks(s.mode);
     const unsigned grid = static_cast<unsigned>(std::min<int64_t>((items + per - 1) / per, 148 * per_sm));
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    with_mode(s, [&](auto m, auto wd) {
+    with_mode<true>(s, [&](auto m, auto wd) {
         if constexpr (!decltype(wd)::value)  // pieces are no wider than a warp
             with_types(x_type, x_type, [&](auto tx, auto ty) {
                 using TX = decltype(tx);
@@ -374,7 +376,7 @@ tri_attn_status tri_norm_bwd(const tri_norm_bwd_args* a, tri_attn_stream_t strea
     p.db = a->db;
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     if (blocks) {
-        with_mode(s, [&](auto m, auto wd) {
+        with_mode<false>(s, [&](auto m, auto wd) {
             constexpr int MODE = decltype(m)::value;
             constexpr bool WIDE = decltype(wd)::value;
             with_types(f.x_type, f.y_type, [&](auto tx, auto ty) {

@@ -65,8 +65,10 @@ struct NormParams {
 // sixteen, since those that a lane does not have would cost their instructions and
 // registers all the same: 200000 rows of 100 BF16 channels take 36 us forward and
 // 47 us backward in place of 74 and 208, 209 FP32 channels 62 and 86 in place of 78
-// and 105.
-enum : int { kVec = 0, kBy4 = 4, kBy32 = 32, kBy32Half = 33, kBy32Quarter = 34 };
+// and 105.  The 8-bit activation by itself takes rows of 65 to 128 channels by 8
+// lanes (kBy8): 200000 rows of 100 in 27 us in place of 45; with the norm's sums
+// beside it that mode needs too many registers (backward 72 us).
+enum : int { kVec = 0, kBy4 = 4, kBy8 = 8, kBy32 = 32, kBy32Half = 33, kBy32Quarter = 34 };
 // channels per lane, and the lanes' stride where they are not neighbours
 __host__ __device__ constexpr int norm_n(int mode) {
     return mode == kBy32Quarter ? 4 : mode == kBy32Half ? 8 : 16;
@@ -75,7 +77,7 @@ __host__ __device__ constexpr int norm_stride(int mode) { return mode > kBy32 ? 
 template <int MODE>
 __device__ __forceinline__ int norm_col(int g, int k) {
     if constexpr (MODE == kVec) return g * 16 + k;
-    if constexpr (MODE == kBy4) return g + 4 * k;
+    if constexpr (MODE == kBy4 || MODE == kBy8) return g + MODE * k;
     return (g >> 5) * 512 + (g & 31) + 32 * k;
 }
 
@@ -335,19 +337,20 @@ __device__ __forceinline__ void act8_emit(const NormParams& p, int64_t row, bool
         for (int k = 0; k < N; ++k) v[k] = k & 1 ? u[k / 2].y : u[k / 2].x;
 #pragma unroll
         for (int k = 0; k < N; ++k) a[k] = __float_as_uint(v[k]) & 0x7FFFFFFFu;
-        if constexpr (MODE != kBy4) {
+        if constexpr (norm_stride(MODE) == 32) {
 #pragma unroll
             for (int k = 0; k < N; ++k)
-                if (32 * k < C) a[k] = __reduce_max_sync(0xFFFFFFFFu, a[k]);
-        } else {  // a block is eight k of four lanes
+                if (32 * k < p.C) a[k] = __reduce_max_sync(0xFFFFFFFFu, a[k]);
+        } else {  // a block is several k of the row's lanes
+            constexpr int kPer = 32 / norm_stride(MODE);
 #pragma unroll
-            for (int s = 0; s < 16; s += 8) {
+            for (int s = 0; s < N; s += kPer) {
 #pragma unroll
-                for (int k = 1; k < 8; ++k) a[s] = max(a[s], a[s + k]);
-                a[s] = max(a[s], __shfl_xor_sync(0xFFFFFFFFu, a[s], 1));
-                a[s] = max(a[s], __shfl_xor_sync(0xFFFFFFFFu, a[s], 2));
+                for (int k = 1; k < kPer; ++k) a[s] = max(a[s], a[s + k]);
 #pragma unroll
-                for (int k = 1; k < 8; ++k) a[s + k] = a[s];
+                for (int m = 1; m < norm_stride(MODE); m *= 2) a[s] = max(a[s], __shfl_xor_sync(0xFFFFFFFFu, a[s], m));
+#pragma unroll
+                for (int k = 1; k < kPer; ++k) a[s + k] = a[s];
             }
         }
 #pragma unroll
@@ -708,7 +711,7 @@ __global__ void __launch_bounds__(1024) tri_ordered_sum_kernel(const float* __re
 // BF16 channels packed in 36 us instead of 31 (5.2 TB/s; unpacking 27 us, 5.9 TB/s).
 // Element by element, 20011 rows of 209 FP32 channels take 10.5 and 7.5 us, bound
 // by their instructions.
-__host__ __device__ constexpr int act8_blocks(int mode) { return mode == kVec || mode == kBy32Quarter ? 6 : 4; }  // per SM
+__host__ __device__ constexpr int act8_blocks(int mode) { return mode == kVec ? 6 : 4; }  // per SM
 template <typename TX, int ACT, int MODE, bool PACK>
 __global__ void __launch_bounds__(kNormThreads, act8_blocks(MODE))
     tri_act8_kernel(const __grid_constant__ NormParams p) {
