@@ -677,10 +677,11 @@ __global__ void __launch_bounds__(WIDE ? 32 * kNormMaxWarps : kNormThreads, WIDE
 
 // out[i] = sum over q < nparts of part[q][i], i < n: the first n0 of them into
 // out0, the rest into out1.  32 columns by 32 runs of q per block; each run is
-// added in ascending q, the runs in ascending order.
-__global__ void __launch_bounds__(1024) tri_ordered_sum_kernel(const float* __restrict__ part, int nparts, int n,
-                                                               float* __restrict__ out0, int n0,
-                                                               float* __restrict__ out1) {
+// added in ascending q, the runs in ascending order.  part is written while this
+// kernel runs, up to the wait: no __restrict__, which would promise that it does not
+// change and let its loads pass the wait.
+__global__ void __launch_bounds__(1024) tri_ordered_sum_kernel(const float* part, int nparts, int n, float* out0,
+                                                               int n0, float* out1) {
     __shared__ float runs[32][33];
     const int lane = threadIdx.x & 31, run = threadIdx.x >> 5;
     const int i = blockIdx.x * 32 + lane;
