@@ -394,3 +394,16 @@ def test_pending_device_error_stops_the_bias_too():
     finally:
         Bd.tri_attn_set_wait_limit_ns(2_000_000_000)
         Bd.tri_attn_device_error(True)
+
+
+def test_log_edges_reach_the_distance_asked_for():
+    """The last bucket of a side starts at max_distance, for every number of buckets."""
+    pairs = [(1, 1), (1, 2), (1, 100), (1, 2 ** 31 - 1), (2, 2), (2, 7), (3, 3), (16, 128), (20, 200000), (255, 255),
+             (255, 2 ** 31 - 1)]
+    pairs += [(per, far) for per in range(1, 41) for far in range(per, 90, 7)]
+    for per, far in pairs:
+        e = T.relpos_edges_log(per, far, "cpu").tolist()
+        assert e[-1] == far and e == sorted(set(e)) and len(e) == 2 * per and [1 - x for x in reversed(e)] == e
+        if per > 1:  # distance 0 has a bucket of its own
+            assert 0 in e and 1 in e
+    assert T.relpos_edges_log(1, 100, "cpu").tolist() == [-99, 100]

@@ -31,13 +31,14 @@ def relpos_edges_clipped(r: int, device="cuda") -> torch.Tensor:
 def relpos_edges_log(per_side: int, max_distance: int, device="cuda") -> torch.Tensor:
     """Edges of 2 * per_side + 1 buckets: distance 0, and per_side buckets to either side, the
     first half of them one distance each, the others growing geometrically up to the last,
-    which starts at max_distance."""
+    which starts at max_distance.  With per_side 1 the one bucket of a side is the last one, and
+    the nearer distances fall into that of distance 0."""
     if not 1 <= per_side <= 255 or not per_side <= max_distance < 2 ** 31:
         raise B.TriAttnError(B.TRI_ATTN_ERR_SHAPE,
                              f"1 <= per_side <= 255 and per_side <= max_distance < 2**31 are needed, got {per_side}, {max_distance}")
     exact = (per_side + 1) // 2
     steps = per_side - exact
-    up = list(range(1, exact + 1))
+    up = list(range(1, exact + 1)) if steps else [max_distance]
     for k in range(1, steps + 1):
         # least n with (n / exact)^steps >= (max_distance / exact)^k, in whole numbers
         n = int(exact * (max_distance / exact) ** (k / steps))
