@@ -407,3 +407,32 @@ def test_log_edges_reach_the_distance_asked_for():
         if per > 1:  # distance 0 has a bucket of its own
             assert 0 in e and 1 in e
     assert T.relpos_edges_log(1, 100, "cpu").tolist() == [-99, 100]
+
+
+def test_groups_of_their_own_over_shared_positions(monkeypatch):
+    """Without pos_k the keys have the queries' positions, but the groups that were given for them."""
+    seen = []
+    monkeypatch.setattr(T.relpos, "relpos_forward", lambda *a: seen.append(a) or torch.zeros(1, 4, 8, 8, dtype=BF))
+    pos, e, t = torch.arange(8, dtype=I32), T.relpos_edges_clipped(3, "cpu"), torch.zeros(8, 4)
+    gq, gk = pos // 4, pos // 2
+    for kw, want in (({}, (None, None)), ({"group_q": gq}, (gq, gq)), ({"group_q": gq, "group_k": gk}, (gq, gk)),
+                     ({"group_k": gk}, (None, gk)), ({"pos_k": pos, "group_q": gq}, (gq, None))):
+        T.relative_position_bias(t, e, pos, **kw)
+        _, _, pq, pk, got_q, got_k, _ = seen.pop()
+        assert pq is pos and pk is pos and got_q is want[0] and got_k is want[1]
+
+
+@pytest.mark.gpu
+def test_groups_of_their_own_over_shared_positions_on_the_gpu():
+    table, e, _, pk, _, gk, base, d = make(2, 4, 40, 40, "clip", 3, True, F32)
+    gq = gk.flip(1).contiguous()
+    t = table.clone().requires_grad_()
+    bias = T.relative_position_bias(t, e, pk, group_q=gq, group_k=gk, base=base)
+    assert torch.equal(bias, T.relpos_forward(table, e, pk, pk, gq, gk, base))
+    assert not torch.equal(bias, T.relpos_forward(table, e, pk, pk, gq, gq, base))
+    bias.backward(d)
+    assert torch.equal(t.grad, T.relpos_backward(d, e, pk, pk, gq, gk))
+    for kw in ({"group_k": gk}, {"pos_k": pk, "group_q": gq}):  # one of the two alone
+        with pytest.raises(Bd.TriAttnError) as err:
+            T.relative_position_bias(table, e, pk, **kw)
+        assert err.value.status == Bd.TRI_ATTN_ERR_NULL

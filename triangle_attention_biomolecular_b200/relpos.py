@@ -149,8 +149,8 @@ class RelativePositionBiasFunction(torch.autograd.Function):
 
 def relative_position_bias(table, edges, pos_q, pos_k=None, group_q=None, group_k=None,
                            base: Optional[torch.Tensor] = None):
-    """Differentiable relative position bias (see :func:`relpos_forward`); without ``pos_k`` the
-    keys have the queries' positions and groups."""
+    """Differentiable relative position bias (see :func:`relpos_forward`).  Without ``pos_k`` the
+    keys have the queries' positions, and their groups unless ``group_k`` gives others."""
     if pos_k is None:
-        pos_k, group_k = pos_q, group_q
+        pos_k, group_k = pos_q, group_q if group_k is None else group_k
     return RelativePositionBiasFunction.apply(table, base, edges, pos_q, pos_k, group_q, group_k)
