@@ -436,3 +436,41 @@ def test_groups_of_their_own_over_shared_positions_on_the_gpu():
         with pytest.raises(Bd.TriAttnError) as err:
             T.relative_position_bias(table, e, pk, **kw)
         assert err.value.status == Bd.TRI_ATTN_ERR_NULL
+
+
+@pytest.mark.parametrize("N", [8, 9, 21])
+def test_the_bias_can_be_changed_in_place(monkeypatch, N):
+    """Odd rows lie in a padded buffer of which the result must not be a view for autograd, which
+    refuses in-place changes of a view made within a Function."""
+    def forward(table, e, q, k, gq, gk, base, bias):
+        bias.copy_(table[0, :, None, None].expand(bias.shape))
+
+    monkeypatch.setattr(Bd, "tri_relpos_fwd", forward)
+    e, pos = T.relpos_edges_clipped(3, "cpu"), torch.arange(N, dtype=I32)
+    t = torch.ones(7, 4).requires_grad_()
+    bias = T.relative_position_bias(t, e, pos)
+    pad = (N + 7) // 8 * 8
+    assert bias.shape == (1, 4, N, N) and bias.stride()[1:] == (N * pad, pad, 1)
+    assert bias.untyped_storage().nbytes() >= 2 * 4 * N * pad  # the last row's last 16 bytes exist
+    other = torch.full((), 2.0, dtype=BF).requires_grad_()
+    bias += other
+    assert bias.requires_grad and (bias == 3).all()
+    bias.masked_fill_(pos[None, :] > 5, -1e9)
+    monkeypatch.setattr(T.relpos, "relpos_backward", lambda g, *a: g.float().sum((0, 2, 3))[None].expand(7, 4))
+    bias.sum().backward()
+    assert (t.grad == 6 * N).all() and other.grad == 24 * N  # six keys of each row are left, four heads
+    assert bias.detach().stride() == bias.stride()
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("N", [40, 41])
+def test_the_bias_can_be_changed_in_place_on_the_gpu(N):
+    table, e, _, pk, *_, base, d = make(2, 4, N, N, "clip", 0, True, F32)
+    t = table.clone().requires_grad_()
+    bias = T.relative_position_bias(t, e, pk)
+    assert T.relpos._layout(bias).data_ptr() == bias.data_ptr()  # the layout that the kernels read
+    want = bias.detach() + base
+    bias += base
+    assert torch.equal(bias, want)
+    bias.backward(d)
+    assert torch.equal(t.grad, T.relpos_backward(d, e, pk, pk))

@@ -68,10 +68,14 @@ def _layout(t: torch.Tensor) -> torch.Tensor:
 
 
 def _padded(shape, like) -> torch.Tensor:
+    """An uninitialised BF16 tensor whose rows are padded to a multiple of 8.  It is cut to its
+    shape in place: were it a view, autograd would refuse in-place changes of a bias that a
+    Function returns."""
     *lead, n = shape
     if n % 8 == 0:
         return like.new_empty(shape, dtype=torch.bfloat16)
-    return like.new_empty((*lead, (n + 7) // 8 * 8), dtype=torch.bfloat16).narrow(-1, 0, n)
+    t = like.new_empty((*lead, (n + 7) // 8 * 8), dtype=torch.bfloat16)
+    return t.as_strided_(shape, t.stride())
 
 
 def _index(pos_q, pos_k, group_q, group_k, like=None):
