@@ -600,3 +600,25 @@ def test_pending_device_error_stops_the_norm_too():
         Bd.tri_attn_device_error(True)
     Bd.tri_norm_fwd(x, None, None, y, stats)
     assert torch.isfinite(y).all()
+
+
+def test_weight_gradients_are_tensors_of_their_own(lib, monkeypatch):
+    """Not two views of one: those share a version counter and refuse in-place changes."""
+    def backward(x, codes, exps, kind, stats, w, dy, geometry, x_dtype, into, stream, *others):
+        C = geometry[3]
+        for k, at in enumerate(into[2:4]):
+            ctypes.memmove(at, (ctypes.c_float * C)(*[k + 1.0] * C), 4 * C)
+
+    monkeypatch.setattr(Bd, "_norm_bwd", backward)
+    monkeypatch.setattr(Bd, "_norm_fwd", lambda *a: None)
+    x, w, b = torch.randn(4, 8), torch.ones(8, requires_grad=True), torch.ones(8, requires_grad=True)
+    _, dw, db = T.norm_backward(x, torch.zeros(2, 4), x, w)
+    assert (dw == 1).all() and (db == 2).all() and dw.dtype == db.dtype == F32 and dw.shape == db.shape == (8,)
+    assert dw.untyped_storage().data_ptr() != db.untyped_storage().data_ptr()
+    dw.add_(0.5 * w)  # weight decay, say
+    assert dw.requires_grad and not db.requires_grad
+    T.layer_norm(x, w, b).sum().backward()
+    product = (w.grad * torch.ones(8, requires_grad=True)).sum()
+    b.grad.zero_()  # has nothing to do with w.grad, which the product keeps
+    assert w.grad._version == 0
+    product.backward()

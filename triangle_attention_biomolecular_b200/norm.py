@@ -137,12 +137,10 @@ def norm_backward(x, stats, dy, weight=None, need_dx: bool = True, need_dw: Opti
         dx = _empty(dy, x.dtype)
         into[0], into[1] = dx.data_ptr(), C
     if weight is not None if need_dw is None else need_dw:
-        grads = dy.new_empty((2, C), dtype=torch.float32)
-        dw, db = grads.unbind(0)
+        dw, db = dy.new_empty(C, dtype=torch.float32), dy.new_empty(C, dtype=torch.float32)
         need = B.tri_norm_bwd_workspace_bytes(R, C)
         ws = dy.new_empty(need, dtype=torch.uint8)
-        into[2] = grads.data_ptr()
-        into[3:] = into[2] + 4 * C, ws.data_ptr(), need
+        into[2:] = dw.data_ptr(), db.data_ptr(), ws.data_ptr(), need
     if isinstance(x, Act8):
         B._norm_bwd(None, _rows(x.codes), _rows(x.exps), x.kind, stats, _param(weight), dy2, geometry, x.dtype, into, None)
     else:
