@@ -57,13 +57,14 @@ NormShape norm_shape(int C, bool vec, bool alone = false) {
     s.per_block = s.threads / s.lanes;
     return s;
 }
-// blocks of the backward: a function of the sizes and the alignment alone, like every order of
-// additions there
-int64_t norm_bwd_blocks(int64_t R, int C, bool vec) {
+// blocks of the backward: a function of the sizes, the alignment and of whether dw and db are
+// wanted (sums) alone, like every order of additions there
+int64_t norm_bwd_blocks(int64_t R, int C, bool vec, bool sums) {
     const NormShape s = norm_shape(C, vec);
     // few rows: one block goes through them, and the launch that adds up partial sums is saved
-    // (64 rows of 128: 17.5 us of host time and 4.4 us of the device's, against 19.7 and 6.4)
-    if (R > 0 && R <= 4 * s.per_block) return 1;
+    // (64 rows of 128: 17.5 us of host time and 4.4 us of the device's, against 19.7 and 6.4);
+    // without sums there is no such launch (128 rows of 128: 2.2 us, in one block 3.4)
+    if (sums && R > 0 && R <= 4 * s.per_block) return 1;
     return std::min<int64_t>((R + s.per_block - 1) / s.per_block, 148 * (s.lanes > 32 ? 4 : tri::norm_bwd_per_sm(s.mode)));
 }
 
@@ -334,7 +335,7 @@ tri_attn_status tri_norm_restore(const tri_norm_fwd_args* a, tri_attn_stream_t s
 size_t tri_norm_bwd_workspace_bytes(int64_t R, int C) {
     if (check_norm_sizes(R, C)) return 0;
     // never 0 for sizes that are valid
-    const int64_t blocks = std::max(norm_bwd_blocks(R, C, false), norm_bwd_blocks(R, C, true));
+    const int64_t blocks = std::max(norm_bwd_blocks(R, C, false, true), norm_bwd_blocks(R, C, true, true));
     return static_cast<size_t>(std::max<int64_t>(1, blocks)) * 2 * C * sizeof(float);
 }
 
@@ -364,7 +365,7 @@ tri_attn_status tri_norm_bwd(const tri_norm_bwd_args* a, tri_attn_stream_t strea
                      (!a->dx || vec_rows(a->dx, a->dx_stride, xe)) &&
                      (act ? vec_act8(f.act) : vec_rows(f.x, f.x_stride, xe));
     const NormShape s = norm_shape(f.C, vec);
-    const int64_t blocks = norm_bwd_blocks(f.R, f.C, vec);
+    const int64_t blocks = norm_bwd_blocks(f.R, f.C, vec, a->dw != nullptr);
     NormParams p{};
     norm_params(p, f, s);
     p.dy = a->dy;
