@@ -474,3 +474,17 @@ def test_the_bias_can_be_changed_in_place_on_the_gpu(N):
     assert torch.equal(bias, want)
     bias.backward(d)
     assert torch.equal(t.grad, T.relpos_backward(d, e, pk, pk))
+
+
+def test_the_backward_launches_no_more_blocks_than_run_at_once(lib):
+    """Every block costs its zeroed columns, its look-up table and a partial sum.  A block's shared
+    memory (8 warps x buckets x 128 bytes + 6 KB, + 1 KB of its own) fits twice into an SM's 228 KB
+    up to 107 buckets."""
+    for E, per_sm in ((64, 2), (106, 2), (107, 1), (190, 1), (300, 1), (510, 1)):
+        for H, N in ((4, 768), (16, 2048), (1, 4096)):
+            heads = -(-H // 4) if H >= 4 else 1  # blocks of heads, each with its own columns
+            blocks = Bd.tri_relpos_bwd_workspace_bytes(1, H, N, N, E, False) // ((E + 1) * H * 4)
+            assert 0 < blocks <= 148 * per_sm, (E, H, N, blocks)
+            # the rows are cut for the warps that run at once, over all blocks of heads, each of which
+            # may end in a block that is not full
+            assert blocks * heads <= 148 * per_sm + heads, (E, H, N, blocks)

@@ -306,16 +306,17 @@ RelposBwdShape relpos_bwd_shape(int B, int H, int Nq, int Nk, int nb) {
     s.warps = tri::kRelBwdWarps;
     while (s.warps > 1 && tri::relpos_bwd_smem(nb, s.warps) > tri::kRelBwdSmem) --s.warps;
     s.smem = tri::relpos_bwd_smem(nb, s.warps);
+    const int64_t at_once = 148 * tri::relpos_bwd_per_sm(s.smem);  // blocks
     // as many tasks as warps run at once, each with at least one batch of rows; those with many
     // take two in a row, so that the buckets in hand last longer
-    const int64_t want = std::max<int64_t>(1, 148 * tri::kRelBwdBlocks * s.warps / (tiles * s.head_blocks));
+    const int64_t want = std::max<int64_t>(1, at_once * s.warps / (tiles * s.head_blocks));
     const int64_t batches = (Nq + tri::kRelRows - 1) / tri::kRelRows;
     s.row_tasks = static_cast<int>(std::min(want, batches));
     s.run = static_cast<int>(std::min<int64_t>(2, batches / s.row_tasks));
     const int64_t tasks = tiles * s.row_tasks;  // < 2^31: at most one per warp at once, or B * chunks of them
     // a few tasks: one block, as in the norm (64 x 64 x 4 heads: 17 us of host time, the device's
     // 12.6 us, against 19 and 10.5)
-    const int64_t blocks = std::min<int64_t>((tasks + s.warps - 1) / s.warps, 148 * tri::kRelBwdBlocks);
+    const int64_t blocks = std::min<int64_t>((tasks + s.warps - 1) / s.warps, at_once);
     s.grid = tasks <= 4 * s.warps ? 1u : static_cast<unsigned>(blocks);
     return s;
 }

@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(kRelThreads, kRelFwdBlocks)
 //
 // 2048 x 2048 x 16 heads: 55 us (44 us in one chain without gaps; floor 20.4 us).
 // What bounds it is the latency of 16 warps per SM, as many as the columns and the
-// registers leave room for; 24 warps spilled and took 98 us, and so did batches of
+// registers leave room for (8 from 108 buckets on, fewer from 193 on); 24 warps spilled and took 98 us, and so did batches of
 // two rows.  2 x 1031 x 1031 x 12 heads with edges out to 200000: 39 us, of which 17
 // are rows gone through one by one.  768 x 768 x 4 heads: 11 us, most of it latency.
 constexpr int kRelBwdWarps = 8, kRelBwdBlocks = 2;  // per block, blocks per SM
@@ -333,6 +333,12 @@ constexpr int kRelBwdSmem = 200 * 1024;  // the columns of as many warps as fit
 
 __host__ constexpr size_t relpos_bwd_smem(int nb, int warps) {
     return static_cast<size_t>(warps) * nb * 32 * 4 + 512 * 4 + kRelLut * 2;
+}
+// blocks that an SM holds at once: two while the columns leave room for a second one (up to 107
+// buckets), then one; a block takes 1 KB more than it asks for.  768 x 768 x 4 heads with 129
+// buckets: 11.2 us; cut for two blocks where one fits, 17.6
+__host__ constexpr int relpos_bwd_per_sm(size_t smem) {
+    return kRelBwdBlocks * (smem + 1024) <= 228 * 1024 ? kRelBwdBlocks : 1;
 }
 
 __device__ __forceinline__ int relpos_cut(int64_t v) {
