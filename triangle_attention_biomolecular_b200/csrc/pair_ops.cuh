@@ -428,8 +428,10 @@ tri_attn_status tri_relpos_fwd(const tri_relpos_fwd_args* a, tri_attn_stream_t s
     }
     // all blocks run at once, and hold at least one row of chunks
     const int64_t items = static_cast<int64_t>(a->B) * a->Nq * p.chunks, threads = tri::kRelThreads;
-    // few rows: the heads go to blocks of their own, four at least (one row of 4096 keys with 16
-    // heads runs on 8 blocks in place of 2)
+    // few rows: the heads go to blocks of their own, more than four halved, which leaves two to four
+    // (one row of 4096 keys with 16 heads runs on 8 blocks in place of 2).  Table entries hold four
+    // heads, but keeping to fours gains nothing: 8 x 64 with 5 heads and a base 4.0 us, by fours 4.8;
+    // one row of 4096 keys with 12 heads 4.0 either way
     while (p.heads > 4 && (items + threads - 1) / threads * ((a->H + p.heads - 1) / p.heads) < 74) p.heads /= 2;
     const unsigned head_blocks = (a->H + p.heads - 1) / p.heads;
     const int64_t at_once =

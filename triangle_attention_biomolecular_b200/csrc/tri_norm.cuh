@@ -420,7 +420,10 @@ struct NormRow8 {
 constexpr int kNormThreads = 256;   // rows of up to 512 channels: 256 / G of them per block
 constexpr int kNormMaxWarps = 16;   // rows of up to 8192 channels: one block, a warp per 512
 // Blocks per SM.  A row on its way takes eight registers in BF16 and sixteen in FP32 or element by
-// element, so those get the registers of a block less.
+// element, so those get the registers of a block less.  The 8-bit form beside it does not fit the 80
+// registers that kBy32 has then and spills 80 to 88 bytes.  Two blocks without spills do better from
+// FP32 (100000 rows of 387 with the int8 form 93 us in place of 110) and worse from BF16 (151 and
+// 126) and without the 8-bit form (60 and 52; BF16 111 and 78).
 __host__ __device__ constexpr int norm_fwd_blocks(int mode, bool f32) {
     return mode == kBy32Quarter ? 5 : mode == kBy32Half || (mode == kVec && !f32) ? 4 : 3;
 }

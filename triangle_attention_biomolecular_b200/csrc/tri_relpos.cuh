@@ -324,9 +324,10 @@ __global__ void __launch_bounds__(kRelThreads, kRelFwdBlocks)
 //
 // 2048 x 2048 x 16 heads: 55 us (44 us in one chain without gaps; floor 20.4 us).
 // What bounds it is the latency of 16 warps per SM, as many as the columns and the
-// registers leave room for (8 from 108 buckets on, fewer from 193 on); 24 warps spilled and took 98 us, and so did batches of
-// two rows.  2 x 1031 x 1031 x 12 heads with edges out to 200000: 39 us, of which 17
-// are rows gone through one by one.  768 x 768 x 4 heads: 11 us, most of it latency.
+// registers leave room for (8 from 108 buckets on, fewer from 195 on); 24 warps
+// spilled and took 98 us, and so did batches of two rows.  2 x 1031 x 1031 x 12 heads
+// with edges out to 200000: 39 us, of which 17 are rows gone through one by one.
+// 768 x 768 x 4 heads: 11 us, most of it latency.
 constexpr int kRelBwdWarps = 8, kRelBwdBlocks = 2;  // per block, blocks per SM
 constexpr int kRelRows = 4;
 constexpr int kRelBwdSmem = 200 * 1024;  // the columns of as many warps as fit
