@@ -622,3 +622,106 @@ def test_weight_gradients_are_tensors_of_their_own(lib, monkeypatch):
     b.grad.zero_()  # has nothing to do with w.grad, which the product keeps
     assert w.grad._version == 0
     product.backward()
+
+
+# rows that are walked element by element, in each way that lanes share them (4 lanes, a warp with
+# four, eight or sixteen channels per lane, a block), and rows in vectors: three rounds of rows per
+# block and a last one that is not full, forward and backward.  A block's rows per round times the
+# blocks of the largest grid: 28416, 5920, 4736, 3552 and 1184 rows forward, less backward.
+ROUNDS = [  # R, C, x, y, padding of the rows
+    (57011, 33, BF, BF, 0), (57011, 64, F32, BF, 1), (12011, 67, BF, F32, 0), (12011, 128, BF, BF, 1),
+    (9511, 129, F32, F32, 0), (9511, 256, BF, BF, 3), (7211, 257, F32, BF, 0), (7211, 387, BF, BF, 0),
+    (7211, 512, F32, F32, 1), (2411, 513, F32, F32, 0), (2411, 1025, BF, BF, 0), (2411, 1024, BF, F32, 1),
+    (2411, 1024, BF, BF, 0), (38011, 128, F32, F32, 0),
+]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kept", [None, "int8", "e4m3"])
+@pytest.mark.parametrize("R,C,xt,yt,pad", ROUNDS)
+def test_many_rounds_of_rows(R, C, xt, yt, pad, kept):
+    x, dy = make(R, C, xt, 7 * R + C, pad), make(R, C, yt, R + 3 * C, pad)
+    w, b = 1 + 0.3 * make(1, C, F32, C)[0], make(1, C, F32, C + 1)[0]
+    y, stats, a = T.norm_forward(x, w, b, out_dtype=yt, checkpoint=kept)
+    again, xk = None, x
+    if kept:
+        again, xk = T.norm_restore(a, stats, w, b, out_dtype=yt), T.act8_unpack(a, F32)
+        packed = T.act8_pack(x, kept)
+        assert torch.equal(packed.codes.view(torch.uint8), a.codes.view(torch.uint8)) and torch.equal(packed.exps, a.exps)
+    dx, dw, db = T.norm_backward(a if kept else x, stats, dy, w)
+    # a thread adds 4 rows at most here, then the partial sums: within check_norm's counts
+    check_norm(x, xk, w, b, stats, y, again, dy, dx, dw, db)
+    # the same rows in calls of one round, bit for bit
+    step = {True: 592, False: 2368}[C > 512]
+    for r in range(0, R, step):
+        s = slice(r, min(R, r + step))
+        y1, s1, a1 = T.norm_forward(x[s], w, b, out_dtype=yt, checkpoint=kept)
+        assert torch.equal(y[s], y1) and torch.equal(stats[:, s], s1)
+        if kept:
+            assert torch.equal(a.codes[s].view(torch.uint8), a1.codes.view(torch.uint8)) and torch.equal(a.exps[s], a1.exps)
+            assert torch.equal(again[s], T.norm_restore(a1, s1, w, b, out_dtype=yt))
+            assert torch.equal(xk[s], T.act8_unpack(a1, F32))
+        assert torch.equal(dx[s], T.norm_backward(a1 if kept else x[s], s1, dy[s], w, need_dw=False)[0])
+
+
+def guarded(R, C, dtype, fill, align):
+    """A buffer full of ``fill`` and the [R, C] rows within it that a call may write: rows of a
+    multiple of 32 bytes with something before and behind each, or rows at an odd element."""
+    width = (C + 31) // 32 * 32 + 64
+    buf = torch.full((R + 2, width if align else width + 1), fill, dtype=dtype, device="cuda")
+    at = 32 if align else 3
+    rows = buf[1:-1, at:at + C]
+    if align:
+        assert rows.data_ptr() % 32 == 0 and rows.stride(0) * rows.element_size() % 32 == 0
+    return buf, rows
+
+
+def untouched(buf, rows, fill):
+    rows.fill_(fill)
+    b = buf.float()
+    return bool(torch.isnan(b).all() if fill != fill else (b == fill).all())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("align", [True, False])
+@pytest.mark.parametrize("t", [BF, F32])
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("C", [16, 48, 100, 112, 128, 209, 512, 528, 640, 1025])
+def test_every_output_leaves_what_lies_around_it(C, kind, t, align):
+    """y, the 8-bit form, the restored y, dx, dw, db, the workspace and unpacked values, in rows of
+    vectors (C a multiple of 16, align) where lanes exceed the row, and element by element."""
+    R, nan = 37, float("nan")
+    k, dt = T.norm._KINDS[kind]
+    fill = 99 if kind == "int8" else 96  # 96 is an e4m3 number
+    x, dy = (guarded(R, C, t, 0, align)[1].copy_(make(R, C, t, s)) for s in (C, C + 1))
+    w = 1 + 0.3 * make(1, C, F32, C)[0]
+    want_y, want_stats, want = T.norm_forward(x, w, checkpoint=kind)
+    want_dx, want_dw, want_db = T.norm_backward(want, want_stats, dy, w)
+    (yb, y), (cb, codes) = guarded(R, C, t, nan, align), guarded(R, C, dt, fill, align)
+    eb, exps = guarded(R, (C + 31) // 32, torch.uint8, 77, align)
+    stats = torch.full((2 * R + 8,), nan, device="cuda")
+    Bd.tri_norm_fwd(x, w, None, y, stats[4:-4].view(2, R), codes, exps, k)
+    assert torch.equal(y, want_y) and torch.equal(stats[4:-4].view(2, R), want_stats)
+    assert torch.equal(codes.float(), want.codes.float()) and torch.equal(exps, want.exps)
+    rb, again = guarded(R, C, t, nan, align)
+    Bd.tri_norm_restore(codes, exps, k, want_stats, w, None, again)
+    assert torch.equal(again, T.norm_restore(want, want_stats, w))
+    ub, values = guarded(R, C, t, nan, align)
+    Bd.tri_act8_unpack(codes, exps, k, values)
+    assert torch.equal(values, T.act8_unpack(want))
+    db_, dx = guarded(R, C, t, nan, align)
+    need = Bd.tri_norm_bwd_workspace_bytes(R, C)
+    ws = torch.full((need + 64,), 90, dtype=torch.uint8, device="cuda")
+    sums = torch.full((2 * C + 12,), nan, device="cuda")
+    dw, db = sums[4:C + 4], sums[C + 8:-4]
+    Bd.tri_norm_bwd(None, codes, exps, k, want_stats, w, dy, dx, dw, db, ws[:need])
+    assert torch.equal(dx, want_dx) and torch.equal(dw, want_dw) and torch.equal(db, want_db)
+    assert (ws[need:] == 90).all() and torch.isnan(sums[[0, 1, 2, 3, C + 4, C + 5, C + 6, C + 7, -4, -3, -2, -1]]).all()
+    pb, codes2 = guarded(R, C, dt, fill, align)
+    qb, exps2 = guarded(R, (C + 31) // 32, torch.uint8, 77, align)
+    Bd.tri_act8_pack(x, codes2, exps2, k)
+    assert torch.equal(codes2.float(), want.codes.float()) and torch.equal(exps2, want.exps)
+    for buf, rows, f in ((yb, y, nan), (cb, codes, fill), (eb, exps, 77), (rb, again, nan), (ub, values, nan), (db_, dx, nan),
+                         (pb, codes2, fill), (qb, exps2, 77)):
+        assert untouched(buf, rows, f)
+    assert torch.isnan(stats[:4]).all() and torch.isnan(stats[-4:]).all()
