@@ -488,3 +488,12 @@ def test_the_backward_launches_no_more_blocks_than_run_at_once(lib):
             # the rows are cut for the warps that run at once, over all blocks of heads, each of which
             # may end in a block that is not full
             assert blocks * heads <= 148 * per_sm + heads, (E, H, N, blocks)
+
+
+def test_edges_of_another_shape_are_refused_in_both_directions(lib):
+    pos, t, d = torch.arange(8, dtype=I32), torch.zeros(7, 4), torch.zeros(1, 4, 8, 8, dtype=BF)
+    for e in (torch.tensor(3, dtype=I32), torch.zeros(2, 3, dtype=I32)):
+        for call in (lambda: T.relpos_forward(t, e, pos, pos), lambda: T.relpos_backward(d, e, pos, pos)):
+            with pytest.raises(Bd.TriAttnError) as err:
+                call()
+            assert err.value.status == Bd.TRI_ATTN_ERR_SHAPE

@@ -127,7 +127,7 @@ def relpos_backward(dbias, edges, pos_q, pos_k, group_q=None, group_k=None):
     if dbias.dim() != 4:
         raise B.TriAttnError(B.TRI_ATTN_ERR_SHAPE, f"dbias must be [B, H, Nq, Nk], got {list(dbias.shape)}")
     q, k, gq, gk = _index(pos_q, pos_k, group_q, group_k, dbias)
-    E, H = edges.shape[0], dbias.shape[1]
+    E, H = edges.numel(), dbias.shape[1]  # their shape is checked with the others
     dtable = dbias.new_empty((E + 1 + (gq is not None), H), dtype=torch.float32)
     ws = dbias.new_empty(B.tri_relpos_bwd_workspace_bytes(q.shape[0], H, q.shape[1], k.shape[1], E, gq is not None),
                          dtype=torch.uint8)
