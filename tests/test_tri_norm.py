@@ -725,3 +725,14 @@ def test_every_output_leaves_what_lies_around_it(C, kind, t, align):
                          (pb, codes2, fill), (qb, exps2, 77)):
         assert untouched(buf, rows, f)
     assert torch.isnan(stats[:4]).all() and torch.isnan(stats[-4:]).all()
+
+
+def test_eps_past_fp32_is_refused(lib):
+    """Like an infinite one, with the library's own error."""
+    x = torch.zeros(4, 8)
+    for eps in (1e39, float("inf"), float("nan"), -1.0):
+        for call in (lambda: T.norm_forward(x, eps=eps), lambda: T.layer_norm(x, eps=eps),
+                     lambda: T.norm_linear(x, None, None, torch.zeros(3, 8), eps=eps)):
+            with pytest.raises(Bd.TriAttnError) as e:
+                call()
+            assert e.value.status == Bd.TRI_ATTN_ERR_SHAPE

@@ -647,6 +647,8 @@ def _workspace(t):
 def _norm_fwd(x, geometry, w, b, y, yp, ys, sp, act, eps, stream, *others) -> None:
     """tri_norm_fwd for outputs that are known to fit: geometry is _rows of x."""
     xp, xs, R, C = geometry
+    if not 0 <= eps <= 3.4e38:  # past FP32 it cannot be handed over at all
+        raise TriAttnError(TRI_ATTN_ERR_SHAPE, f"eps must be finite in FP32 and not negative, got {eps}")
     wp, bp, wt = _affine(w, b, C)
     a = _NORM_PACK.pack(R, xp, xs, wp, bp, yp, ys, sp, *act, C, _float_type(x, "x"), wt, _float_type(y, "y"), eps)
     _call((_lib or load()).tri_norm_fwd, a, "tri_norm_fwd", stream, x, w, b, *others)
