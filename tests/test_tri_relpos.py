@@ -497,3 +497,22 @@ def test_edges_of_another_shape_are_refused_in_both_directions(lib):
             with pytest.raises(Bd.TriAttnError) as err:
                 call()
             assert err.value.status == Bd.TRI_ATTN_ERR_SHAPE
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("r", [52, 53, 54, 96, 97, 128, 255])
+@pytest.mark.parametrize("B,H,N", [(1, 4, 771), (2, 12, 300)])
+def test_many_buckets_are_summed_exactly(B, H, N, r):
+    """Tables around the sizes at which an SM holds one block in place of two, and a block fewer
+    warps (107 and 194 buckets): sums of small whole numbers are exact."""
+    g = torch.Generator().manual_seed(r * N)
+    pos = torch.cumsum(1 + (torch.rand(N, generator=g) < 0.1).int() * 40, 0).int()
+    grp = (torch.arange(N) * 3 // N).int()
+    d = torch.randint(-8, 9, (B, H, N, (N + 7) // 8 * 8), generator=g).to(BF)[..., :N]
+    k = ((pos[None] - pos[:, None]).clamp(-r, r) + r).numpy()
+    for gq in (None, grp):
+        kk = k if gq is None else np.where(grp[:, None] == grp[None], k, 2 * r + 1)
+        kk = np.broadcast_to(kk, (B, N, N))
+        cu = lambda t: None if t is None else t.cuda()  # noqa: E731
+        got = T.relpos_backward(d.cuda(), T.relpos_edges_clipped(r), cu(pos), cu(pos), cu(gq), cu(gq))
+        np.testing.assert_array_equal(f64(got), O.relpos_bwd(f64(d), kk, 2 * r + 1 + (gq is not None)))
