@@ -4,8 +4,9 @@
 tensor and is differentiable in all three.  With ``checkpoint="int8"`` or
 ``"e4m3"`` the forward keeps x in 8 bits (1.03 bytes a value in place of 2 or 4)
 and the backward reads that form.  ``norm_linear`` puts the projection that
-follows into the same step, so that neither x nor the norm's output is kept:
-the backward restores the output from the 8-bit x and the row statistics.
+follows into the same autograd step, so that neither x nor the norm's output is
+kept: the backward restores the output from the 8-bit x and the row statistics.
+It saves memory; the norm and the product (torch.matmul) are launches of their own.
 
 The 8-bit form (:class:`Act8`): 32 neighbouring channels share a power-of-two
 scale, the least under which the block's largest magnitude fits the code range

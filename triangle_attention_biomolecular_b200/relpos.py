@@ -10,6 +10,9 @@ different groups takes the table's last row.  :func:`relpos_edges_clipped` and
 ``triangle_attention`` reads, is differentiable in the table and in ``base`` (a
 bias to add to, such as a projected pair bias), and gives the table's gradient
 in one pass over the bias's, with no atomics: repeated runs are bitwise equal.
+To capture a training step into a CUDA graph, run it once on a side stream first,
+and with no autograd graph of an earlier eager step on the same leaves alive, as
+for the norm.
 """
 from __future__ import annotations
 
